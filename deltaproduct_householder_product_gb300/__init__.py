@@ -13,6 +13,9 @@ from ._lib import DPError, STATE_EXPORT, STATE_IMPORT, STATE_ZERO  # noqa: F401
 
 __all__ = ["forward", "forward_varlen", "forward_noalloc", "forward_path", "supports", "decode_step", "state_io", "check_status",
            "backward", "backward_varlen", "prologue", "prologue_flags", "osdn_write_keys", "forward_write_keys",
+           "linear_attention", "linear_attention_varlen", "linear_attention_step", "linear_attention_backward",
+           "linear_attention_backward_varlen", "linear_attention_workspace_size", "group_norm",
+           "group_norm_backward", "group_norm_workspace_size",
            "workspace_size", "set_wait_fault",
            "DPError", "abi_version"]
 
@@ -360,6 +363,250 @@ def forward_write_keys(q, k, kw, v, beta, g=None, h0=None, *, impl="auto", out=N
         workspace.numel() * workspace.element_size(), _lib._stream(stream))
     _lib._check(rc, "dp_forward_write_keys")
     return out, h_final
+
+
+def linear_attention_workspace_size(B, T, H, Dk, Dv, *, dtype=torch.bfloat16, impl="auto", max_seqlen=None,
+                                    backward=False):
+    """Device workspace bytes of ``linear_attention`` (or, with ``backward``, of
+    its gradients) for B sequences of T tokens; for the packed calls T is the
+    total and ``max_seqlen`` the longest sequence."""
+    dims = _lib.make_la_dims(B, T, H, Dk, Dv, dtype, impl, max_seqlen or 0)
+    return _lib.sized("dp_linear_attention_backward_workspace_size" if backward
+                      else "dp_linear_attention_workspace_size", dims)
+
+
+def _la_check(lead, q, k, v, log_decay, states, h0, more=()):
+    """Checks shared by the linear-attention calls: lead is the shape of the
+    tokens and heads, ``states`` the number of sequences."""
+    Dk, Dv = q.shape[-1], v.shape[-1]
+    H = lead[-1]
+    dt = q.dtype
+    for name, t, d in (("q", q, Dk), ("k", k, Dk), ("v", v, Dv)) + tuple(more):
+        _lib._need_cuda(name, t, dt)
+        if t.shape != (*lead, d):
+            raise ValueError(f"{name} must be {[*lead, d]}")
+    _lib._need_cuda("log_decay", log_decay, torch.float32)
+    if log_decay.shape != (H,):
+        raise ValueError("log_decay must be [H]")
+    _lib._need_cuda("h0", h0, torch.float32)
+    if h0 is not None and h0.shape != (states, H, Dk, Dv):
+        raise ValueError(f"h0 must be {[states, H, Dk, Dv]}")
+    return Dk, Dv, dt
+
+
+def _la_forward(q, k, v, log_decay, h0, states, cu, max_seqlen, impl, out, h_final, workspace, stream):
+    lead = tuple(q.shape[:-1])
+    Dk, Dv, dt = _la_check(lead, q, k, v, log_decay, states, h0)
+    H, T = lead[-1], lead[-2]
+    dims = _lib.make_la_dims(states, T, H, Dk, Dv, dt, impl, max_seqlen)
+    if out is None:
+        out = torch.empty((*lead, Dv), dtype=dt, device=q.device)
+    _lib._need_cuda("out", out, dt)
+    if out.shape != (*lead, Dv):
+        raise ValueError(f"out must be {[*lead, Dv]}")
+    if h_final is True:
+        h_final = torch.empty((states, H, Dk, Dv), dtype=torch.float32, device=q.device)
+    elif h_final is False:
+        h_final = None
+    _lib._need_cuda("h_final", h_final, torch.float32)
+    if h_final is not None and h_final.shape != (states, H, Dk, Dv):
+        raise ValueError(f"h_final must be {[states, H, Dk, Dv]}")
+    if workspace is None:
+        workspace = torch.zeros(_lib.sized("dp_linear_attention_workspace_size", dims), dtype=torch.uint8,
+                                device=q.device)
+    _lib._need_cuda("workspace", workspace)
+    p, size = _lib._ptr, workspace.numel() * workspace.element_size()
+    if cu is None:
+        rc = _lib.lib().dp_linear_attention(dims, p(q), p(k), p(v), p(log_decay), p(h0), p(out), p(h_final),
+                                            p(workspace), size, _lib._stream(stream))
+        _lib._check(rc, "dp_linear_attention")
+    else:
+        rc = _lib.lib().dp_linear_attention_varlen(dims, p(cu), p(q), p(k), p(v), p(log_decay), p(h0), p(out),
+                                                   p(h_final), p(workspace), size, _lib._stream(stream))
+        _lib._check(rc, "dp_linear_attention_varlen")
+    return out, h_final
+
+
+def linear_attention(q, k, v, log_decay, h0=None, *, impl="auto", out=None, h_final=True, workspace=None,
+                     stream=None):
+    """Linear attention with a decay for each head over whole sequences:
+    S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T, o_t = S_t^T q_t.
+
+    q, k [B,T,H,Dk], v [B,T,H,Dv], CUDA tensors of one dtype (float32 or
+    bfloat16); log_decay [H] float32 (<= 0; no gradient); h0 [B,H,Dk,Dv]
+    float32 or None (zeros). ``out``, ``h_final``, ``workspace``, ``stream``
+    as for ``forward``; ``impl`` "auto", "recurrent" (the CUDA-core kernel) or
+    "chunk_tc" (the tensor-core kernel, bfloat16). Returns (o, h_final_or_None).
+    """
+    if q.dim() != 4:
+        raise ValueError("q must be [B,T,H,Dk]")
+    return _la_forward(q, k, v, log_decay, h0, q.shape[0], None, 0, impl, out, h_final, workspace, stream)
+
+
+def _packed(q, cu_seqlens, max_seqlen):
+    if q.dim() != 3:
+        raise ValueError("q must be [T,H,Dk]")
+    _lib._need_cuda("cu_seqlens", cu_seqlens, torch.int32)
+    N, T = cu_seqlens.numel() - 1, q.shape[0]
+    if N < 0:
+        raise ValueError("cu_seqlens needs at least one entry")
+    if max_seqlen is None:
+        max_seqlen = int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item()) if N > 0 else 0
+    return N, max(int(max_seqlen), 1 if T > 0 else 0)
+
+
+def linear_attention_varlen(q, k, v, log_decay, h0=None, *, cu_seqlens, max_seqlen=None, impl="auto", out=None,
+                            h_final=True, workspace=None, stream=None):
+    """``linear_attention`` over N sequences packed along T: q, k [T,H,Dk],
+    v [T,H,Dv], cu_seqlens int32 [N+1], h0 and h_final [N,H,Dk,Dv].
+    ``max_seqlen`` bounds the longest sequence (read from cu_seqlens when
+    None, which synchronises)."""
+    N, max_seqlen = _packed(q, cu_seqlens, max_seqlen)
+    return _la_forward(q, k, v, log_decay, h0, N, cu_seqlens, max_seqlen, impl, out, h_final, workspace, stream)
+
+
+def linear_attention_step(q, k, v, log_decay, state, *, out=None, stream=None):
+    """One token on a carried fp32 state, updated in place: q, k [B,H,Dk],
+    v [B,H,Dv], state [B,H,Dk,Dv] float32. Returns o [B,H,Dv]."""
+    if q.dim() != 3:
+        raise ValueError("q must be [B,H,Dk]")
+    B, H, _ = q.shape
+    if state is None:
+        raise ValueError("state is required")
+    Dk, Dv, dt = _la_check((B, H), q, k, v, log_decay, B, state)
+    if out is None:
+        out = torch.empty((B, H, Dv), dtype=dt, device=q.device)
+    _lib._need_cuda("out", out, dt)
+    if out.shape != (B, H, Dv):
+        raise ValueError("out must be [B,H,Dv]")
+    dims, p = _lib.make_la_dims(B, 1, H, Dk, Dv, dt), _lib._ptr
+    _lib._check(_lib.lib().dp_linear_attention_step(dims, p(q), p(k), p(v), p(log_decay), p(state), p(out),
+                                                    _lib._stream(stream)), "dp_linear_attention_step")
+    return out
+
+
+def _la_backward(q, k, v, log_decay, h0, states, cu, max_seqlen, d_o, dh_final, want_dh0, impl, workspace, stream):
+    lead = tuple(q.shape[:-1])
+    Dk, Dv, dt = _la_check(lead, q, k, v, log_decay, states, h0, more=(("d_o", d_o, v.shape[-1]),))
+    H, T = lead[-1], lead[-2]
+    _lib._need_cuda("dh_final", dh_final, torch.float32)
+    if dh_final is not None and dh_final.shape != (states, H, Dk, Dv):
+        raise ValueError(f"dh_final must be {[states, H, Dk, Dv]}")
+    dims = _lib.make_la_dims(states, T, H, Dk, Dv, dt, impl, max_seqlen)
+    g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+         "dh0": torch.empty((states, H, Dk, Dv), dtype=torch.float32, device=q.device) if want_dh0 else None}
+    if workspace is None:
+        workspace = torch.zeros(_lib.sized("dp_linear_attention_backward_workspace_size", dims), dtype=torch.uint8,
+                                device=q.device)
+    _lib._need_cuda("workspace", workspace)
+    p, size = _lib._ptr, workspace.numel() * workspace.element_size()
+    args = [p(q), p(k), p(v), p(log_decay), p(h0), p(d_o), p(dh_final), p(g["dq"]), p(g["dk"]), p(g["dv"]),
+            p(g["dh0"]), p(workspace), size, _lib._stream(stream)]
+    if cu is None:
+        _lib._check(_lib.lib().dp_linear_attention_backward(dims, *args), "dp_linear_attention_backward")
+    else:
+        _lib._check(_lib.lib().dp_linear_attention_backward_varlen(dims, p(cu), *args),
+                    "dp_linear_attention_backward_varlen")
+    return g
+
+
+def linear_attention_backward(q, k, v, log_decay, h0=None, *, d_o, dh_final=None, want_dh0=True, impl="auto",
+                              workspace=None, stream=None):
+    """Gradients of <d_o, o> + <dh_final, h_final> through ``linear_attention``.
+
+    Inputs as for ``linear_attention``; d_o [B,T,H,Dv] of the inputs' dtype;
+    dh_final float32 [B,H,Dk,Dv] or None (zeros). Returns a dict of dq, dk,
+    dv (the inputs' dtype) and dh0 (float32; None unless ``want_dh0``).
+    """
+    if q.dim() != 4:
+        raise ValueError("q must be [B,T,H,Dk]")
+    return _la_backward(q, k, v, log_decay, h0, q.shape[0], None, 0, d_o, dh_final, want_dh0, impl, workspace,
+                        stream)
+
+
+def linear_attention_backward_varlen(q, k, v, log_decay, h0=None, *, cu_seqlens, max_seqlen=None, d_o,
+                                     dh_final=None, want_dh0=True, impl="auto", workspace=None, stream=None):
+    """``linear_attention_backward`` over packed sequences (the layouts of
+    ``linear_attention_varlen``; dh_final and dh0 are [N,H,Dk,Dv])."""
+    N, max_seqlen = _packed(q, cu_seqlens, max_seqlen)
+    return _la_backward(q, k, v, log_decay, h0, N, cu_seqlens, max_seqlen, d_o, dh_final, want_dh0, impl,
+                        workspace, stream)
+
+
+def _gn_dims(x, weight, bias, groups, act, eps):
+    if x.dim() < 2:
+        raise ValueError("x must be [N, ..., C]")
+    if act not in _lib.ACTS:
+        raise ValueError(f"act must be one of {sorted(_lib.ACTS)}")
+    _lib._need_cuda("x", x, x.dtype)
+    N, C = x.shape[0], x.shape[-1]
+    S = 1
+    for n in x.shape[1:-1]:
+        S *= n
+    for name, t in (("weight", weight), ("bias", bias)):
+        _lib._need_cuda(name, t, x.dtype)
+        if t is not None and t.shape != (C,):
+            raise ValueError(f"{name} must be [C]")
+    return _lib.GnDims(N, S, C, int(groups), _lib._dtype_code(x.dtype), _lib.ACTS[act], float(eps))
+
+
+def group_norm_workspace_size(N, S, C, *, groups, dtype=torch.bfloat16, backward=False):
+    """Device workspace bytes of ``group_norm`` (or, with ``backward``, of its
+    gradients) for x [N,S,C]."""
+    return _lib.sized("dp_group_norm_backward_workspace_size" if backward else "dp_group_norm_workspace_size",
+                      _lib.GnDims(N, S, C, int(groups), _lib._dtype_code(dtype), 0, 0.0))
+
+
+def group_norm(x, weight=None, bias=None, *, groups, eps=1e-5, act="none", out=None, workspace=None, stream=None):
+    """Group norm with an activation, channels last: x [N, ..., C] (float32 or
+    bfloat16), statistics over the middle axes and the C / groups channels of
+    each group; weight, bias [C] of x's dtype or None; ``act`` "none" or
+    "silu". For the norm of each head's output o [B,T,H,D], pass
+    ``o.view(B * T, H * D)`` with ``groups=H``. Returns (y, mean, rstd), the
+    statistics float32 [N, groups]."""
+    dims = _gn_dims(x, weight, bias, groups, act, eps)
+    if out is None:
+        out = torch.empty_like(x)
+    _lib._need_cuda("out", out, x.dtype)
+    if out.shape != x.shape:
+        raise ValueError("out must have the shape of x")
+    stats = torch.empty((2, dims.N, max(dims.G, 0)), dtype=torch.float32, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(_lib.sized("dp_group_norm_workspace_size", dims), dtype=torch.uint8, device=x.device)
+    _lib._need_cuda("workspace", workspace)
+    p, mean, rstd = _lib._ptr, stats[0], stats[1]
+    _lib._check(_lib.lib().dp_group_norm(dims, p(x), p(weight), p(bias), p(out), p(mean), p(rstd), p(workspace),
+                                         workspace.numel() * workspace.element_size(), _lib._stream(stream)),
+                "dp_group_norm")
+    return out, mean, rstd
+
+
+def group_norm_backward(dy, x, weight, bias, mean, rstd, *, groups, act="none", workspace=None, stream=None):
+    """Gradients of <dy, y> through ``group_norm``: dy and x [N, ..., C], mean
+    and rstd [N, groups] float32 as ``group_norm`` returned them. Returns a
+    dict of dx (x's dtype), dweight and dbias (float32 [C]; None where the
+    weight or bias is None)."""
+    dims = _gn_dims(x, weight, bias, groups, act, 0.0)
+    _lib._need_cuda("dy", dy, x.dtype)
+    if dy.shape != x.shape:
+        raise ValueError("dy must have the shape of x")
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _lib._need_cuda(name, t, torch.float32)
+        if t.shape != (dims.N, dims.G):
+            raise ValueError(f"{name} must be [N, groups]")
+    g = {"dx": torch.empty_like(x)}
+    for name, t in (("dweight", weight), ("dbias", bias)):
+        g[name] = None if t is None else torch.empty(dims.C, dtype=torch.float32, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(_lib.sized("dp_group_norm_backward_workspace_size", dims), dtype=torch.uint8,
+                                device=x.device)
+    _lib._need_cuda("workspace", workspace)
+    p = _lib._ptr
+    _lib._check(_lib.lib().dp_group_norm_backward(dims, p(dy), p(x), p(weight), p(bias), p(mean), p(rstd),
+                                                  p(g["dx"]), p(g["dweight"]), p(g["dbias"]), p(workspace),
+                                                  workspace.numel() * workspace.element_size(),
+                                                  _lib._stream(stream)), "dp_group_norm_backward")
+    return g
 
 
 def state_io(op, state, ext=None, transposed=False, stream=None):

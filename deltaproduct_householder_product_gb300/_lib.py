@@ -33,6 +33,17 @@ class Dims(ctypes.Structure):
                 ("max_seqlen", ctypes.c_int), ("prologue", ctypes.c_int)]
 
 
+class LaDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
+                ("Dk", ctypes.c_int), ("Dv", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("impl", ctypes.c_int), ("max_seqlen", ctypes.c_int)]
+
+
+class GnDims(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("S", ctypes.c_int), ("C", ctypes.c_int), ("G", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("act", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
 _LIB = None
 _vp = ctypes.c_void_p
 
@@ -65,6 +76,24 @@ def lib():
             [_vp, _vp, _vp]
         L.dp_forward_write_keys.argtypes = [ctypes.POINTER(Dims)] + [_vp] * 10 + [ctypes.c_size_t, _vp]
         L.dp_test_set_wait_fault.argtypes = [ctypes.c_int, ctypes.c_uint]
+        la, gn, size = ctypes.POINTER(LaDims), ctypes.POINTER(GnDims), ctypes.POINTER(ctypes.c_size_t)
+        L.dp_linear_attention_workspace_size.argtypes = [la, size]
+        L.dp_linear_attention_backward_workspace_size.argtypes = [la, size]
+        L.dp_linear_attention.argtypes = [la] + [_vp] * 8 + [ctypes.c_size_t, _vp]
+        L.dp_linear_attention_varlen.argtypes = [la] + [_vp] * 9 + [ctypes.c_size_t, _vp]
+        L.dp_linear_attention_step.argtypes = [la] + [_vp] * 7
+        L.dp_linear_attention_backward.argtypes = [la] + [_vp] * 12 + [ctypes.c_size_t, _vp]
+        L.dp_linear_attention_backward_varlen.argtypes = [la] + [_vp] * 13 + [ctypes.c_size_t, _vp]
+        L.dp_group_norm_workspace_size.argtypes = [gn, size]
+        L.dp_group_norm_backward_workspace_size.argtypes = [gn, size]
+        L.dp_group_norm.argtypes = [gn] + [_vp] * 7 + [ctypes.c_size_t, _vp]
+        L.dp_group_norm_backward.argtypes = [gn] + [_vp] * 10 + [ctypes.c_size_t, _vp]
+        for name in ("dp_linear_attention_workspace_size", "dp_linear_attention_backward_workspace_size",
+                     "dp_linear_attention", "dp_linear_attention_varlen", "dp_linear_attention_step",
+                     "dp_linear_attention_backward", "dp_linear_attention_backward_varlen",
+                     "dp_group_norm_workspace_size", "dp_group_norm_backward_workspace_size", "dp_group_norm",
+                     "dp_group_norm_backward"):
+            getattr(L, name).restype = ctypes.c_int
         for name in ("dp_forward_workspace_size", "dp_forward_workspace_size_fast", "dp_forward_path",
                      "dp_forward", "dp_forward_varlen", "dp_decode_step",
                      "dp_state_io", "dp_check_status", "dp_forward_noalloc",
@@ -152,5 +181,20 @@ def workspace_size(dims, fast=False):
     """dp_forward_workspace_size, or dp_forward_workspace_size_fast if ``fast``."""
     n = ctypes.c_size_t(0)
     name = "dp_forward_workspace_size_fast" if fast else "dp_forward_workspace_size"
+    _check(getattr(lib(), name)(ctypes.byref(dims), ctypes.byref(n)), name)
+    return n.value
+
+
+ACTS = {"none": 0, "silu": 1}
+
+
+def make_la_dims(B, T, H, Dk, Dv, dtype, impl="auto", max_seqlen=0):
+    return LaDims(B, T, H, Dk, Dv, _dtype_code(dtype), IMPLS[impl] if isinstance(impl, str) else int(impl),
+                  max_seqlen)
+
+
+def sized(name, dims):
+    """The byte count that the query ``name`` answers for ``dims``."""
+    n = ctypes.c_size_t(0)
     _check(getattr(lib(), name)(ctypes.byref(dims), ctypes.byref(n)), name)
     return n.value

@@ -2,7 +2,9 @@
 // See include/dp.h for the contract of every entry point.
 #include <string.h>
 
+#include "group_norm.h"
 #include "internal.h"
+#include "linear_attn.h"
 
 namespace {
 
@@ -481,3 +483,272 @@ extern "C" dp_status dp_forward_write_keys(const dp_dims *dims, const void *q, c
     if ((size_t)p.B * p.H == 0) return DP_OK;
     return from_cuda(tc ? dp::launch_chunk_tc(p) : dp::launch_recurrent(p));
 }
+
+// ---------------------------------------------------------------- linear attention
+namespace {
+
+dp_status check_la_dims(const dp_la_dims *d, bool step, bool varlen)
+{
+    if (!d) return DP_ERR_INVALID_ARG;
+    if (d->B < 0 || d->H < 0 || (!step && d->T < 0) || d->max_seqlen < 0) return DP_ERR_INVALID_ARG;
+    if (d->dtype != DP_F32 && d->dtype != DP_BF16) return DP_ERR_INVALID_ARG;
+    if (d->impl < DP_IMPL_AUTO || d->impl > DP_IMPL_CHUNK_TC) return DP_ERR_INVALID_ARG;
+    if (!varlen && d->max_seqlen != 0) return DP_ERR_INVALID_ARG;
+    if (varlen && (d->max_seqlen > d->T || (d->T > 0 && d->max_seqlen < 1))) return DP_ERR_INVALID_ARG;
+    if (!supported_dim(d->Dk) || !supported_dim(d->Dv)) return DP_ERR_UNSUPPORTED;
+    // the grid is one CTA per sequence, head and segment
+    if ((long long)d->B * d->H * dp::kLaMaxCluster > 0x7fffffffll) return DP_ERR_UNSUPPORTED;
+    if (d->impl == DP_IMPL_CHUNK_TC) return DP_ERR_UNSUPPORTED;
+    return DP_OK;
+}
+
+bool la_varlen(const dp_la_dims *d) { return d && d->max_seqlen != 0; }
+
+int la_cluster(const dp_la_dims *d)
+{
+    return dp::la_simt_cluster(d->B, d->H, d->max_seqlen > 0 ? d->max_seqlen : d->T);
+}
+
+size_t la_workspace(const dp_la_dims *d)
+{
+    const int P = la_cluster(d);
+    return kStatusBlock + (P > 1 ? (size_t)d->B * d->H * P * d->Dk * d->Dv * sizeof(float) : 0);
+}
+
+dp_status check_workspace(const void *workspace, size_t bytes, size_t need)
+{
+    if (!workspace || bytes < need) return DP_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return DP_ERR_ALIGNMENT;
+    return device_pointer(workspace) ? DP_OK : DP_ERR_INVALID_ARG;
+}
+
+dp::LaPass la_pass(const dp_la_dims *d, const int *cu, const float *log_decay, void *workspace, dp_stream_t stream)
+{
+    dp::LaPass p;
+    memset(&p, 0, sizeof(p));
+    p.N = d->B; p.T = d->T; p.H = d->H; p.Dx = d->Dk; p.Dz = d->Dv;
+    p.dtype = d->dtype;
+    p.log_decay = log_decay;
+    p.cu = cu;
+    p.max_T = d->max_seqlen > 0 ? d->max_seqlen : d->T;
+    p.P = la_cluster(d);
+    p.status = (uint32_t *)workspace;
+    p.part = (float *)((char *)workspace + kStatusBlock);
+    p.stream = (cudaStream_t)stream;
+    return p;
+}
+
+dp_status la_forward(const dp_la_dims *dims, const int *cu, const void *q, const void *k, const void *v,
+                     const float *log_decay, const float *h0, void *o, float *h_final, void *workspace,
+                     size_t workspace_bytes, dp_stream_t stream)
+{
+    if ((size_t)dims->B * dims->H == 0) return DP_OK;
+    if (dims->T > 0)
+        for (const void *t : {q, k, v, (const void *)o}) DP_TRY(check_ptr(t, 16));
+    DP_TRY(check_ptr(log_decay, 4));
+    if (cu) DP_TRY(check_ptr(cu, 4));
+    if (h0) DP_TRY(check_ptr(h0, 16));
+    if (h_final) DP_TRY(check_ptr(h_final, 16));
+    DP_TRY(check_workspace(workspace, workspace_bytes, la_workspace(dims)));
+    dp::LaPass p = la_pass(dims, cu, log_decay, workspace, stream);
+    p.x = q; p.y = k; p.z = v; p.out = o;
+    p.init = h0; p.fin = h_final;
+    return from_cuda(dp::launch_la_simt(p));
+}
+
+dp_status la_backward(const dp_la_dims *dims, const int *cu, const void *q, const void *k, const void *v,
+                      const float *log_decay, const float *h0, const void *d_o, const float *dh_final, void *dq,
+                      void *dk, void *dv, float *dh0, void *workspace, size_t workspace_bytes, dp_stream_t stream)
+{
+    if ((size_t)dims->B * dims->H == 0) return DP_OK;
+    if (dims->T > 0)
+        for (const void *t : {q, k, v, d_o, (const void *)dq, (const void *)dk, (const void *)dv})
+            DP_TRY(check_ptr(t, 16));
+    DP_TRY(check_ptr(log_decay, 4));
+    if (cu) DP_TRY(check_ptr(cu, 4));
+    if (h0) DP_TRY(check_ptr(h0, 16));
+    if (dh_final) DP_TRY(check_ptr(dh_final, 16));
+    if (dh0) DP_TRY(check_ptr(dh0, 16));
+    DP_TRY(check_workspace(workspace, workspace_bytes, la_workspace(dims)));
+    const dp::LaPass base = la_pass(dims, cu, log_decay, workspace, stream);
+    dp::LaPass p = base;                      // dq_t = S_t d_o_t
+    p.Dx = dims->Dv; p.Dz = dims->Dk;
+    p.x = d_o; p.y = v; p.z = k; p.out = dq;
+    p.init = h0; p.state_t = true;
+    cudaError_t e = dp::launch_la_simt(p);
+    if (e != cudaSuccess) return from_cuda(e);
+    p.x = v; p.y = d_o; p.z = q; p.out = dk;  // dk_t = G_t v_t
+    p.init = dh_final; p.reverse = true;
+    if ((e = dp::launch_la_simt(p)) != cudaSuccess) return from_cuda(e);
+    p = base;                                 // dv_t = G_t^T k_t, and the only pass that writes dh0
+    p.x = k; p.y = q; p.z = d_o; p.out = dv;
+    p.init = dh_final; p.fin = dh0; p.reverse = true;
+    return from_cuda(dp::launch_la_simt(p));
+}
+
+}  // namespace
+
+extern "C" {
+
+dp_status dp_linear_attention_workspace_size(const dp_la_dims *dims, size_t *bytes)
+{
+    if (!bytes) return DP_ERR_INVALID_ARG;
+    DP_TRY(check_la_dims(dims, false, la_varlen(dims)));
+    *bytes = la_workspace(dims);
+    return DP_OK;
+}
+
+dp_status dp_linear_attention_backward_workspace_size(const dp_la_dims *dims, size_t *bytes)
+{
+    return dp_linear_attention_workspace_size(dims, bytes);
+}
+
+dp_status dp_linear_attention(const dp_la_dims *dims, const void *q, const void *k, const void *v,
+                              const float *log_decay, const float *h0, void *o, float *h_final, void *workspace,
+                              size_t workspace_bytes, dp_stream_t stream)
+{
+    DP_TRY(check_la_dims(dims, false, false));
+    return la_forward(dims, nullptr, q, k, v, log_decay, h0, o, h_final, workspace, workspace_bytes, stream);
+}
+
+dp_status dp_linear_attention_varlen(const dp_la_dims *dims, const int *cu_seqlens, const void *q, const void *k,
+                                     const void *v, const float *log_decay, const float *h0, void *o,
+                                     float *h_final, void *workspace, size_t workspace_bytes, dp_stream_t stream)
+{
+    DP_TRY(check_la_dims(dims, false, true));
+    if ((size_t)dims->B * dims->H > 0 && !cu_seqlens) return DP_ERR_INVALID_ARG;
+    return la_forward(dims, cu_seqlens, q, k, v, log_decay, h0, o, h_final, workspace, workspace_bytes, stream);
+}
+
+dp_status dp_linear_attention_step(const dp_la_dims *dims, const void *q, const void *k, const void *v,
+                                   const float *log_decay, float *state, void *o, dp_stream_t stream)
+{
+    DP_TRY(check_la_dims(dims, true, false));
+    if ((size_t)dims->B * dims->H == 0) return DP_OK;
+    for (const void *t : {q, k, v, (const void *)o, (const void *)state}) DP_TRY(check_ptr(t, 16));
+    DP_TRY(check_ptr(log_decay, 4));
+    const dp::LaStep p{dims->B, dims->H, dims->Dk, dims->Dv, dims->dtype, q, k, v, log_decay, state, o,
+                       (cudaStream_t)stream};
+    return from_cuda(dp::launch_la_step(p));
+}
+
+dp_status dp_linear_attention_backward(const dp_la_dims *dims, const void *q, const void *k, const void *v,
+                                       const float *log_decay, const float *h0, const void *d_o,
+                                       const float *dh_final, void *dq, void *dk, void *dv, float *dh0,
+                                       void *workspace, size_t workspace_bytes, dp_stream_t stream)
+{
+    DP_TRY(check_la_dims(dims, false, false));
+    return la_backward(dims, nullptr, q, k, v, log_decay, h0, d_o, dh_final, dq, dk, dv, dh0, workspace,
+                       workspace_bytes, stream);
+}
+
+dp_status dp_linear_attention_backward_varlen(const dp_la_dims *dims, const int *cu_seqlens, const void *q,
+                                              const void *k, const void *v, const float *log_decay,
+                                              const float *h0, const void *d_o, const float *dh_final, void *dq,
+                                              void *dk, void *dv, float *dh0, void *workspace,
+                                              size_t workspace_bytes, dp_stream_t stream)
+{
+    DP_TRY(check_la_dims(dims, false, true));
+    if ((size_t)dims->B * dims->H > 0 && !cu_seqlens) return DP_ERR_INVALID_ARG;
+    return la_backward(dims, cu_seqlens, q, k, v, log_decay, h0, d_o, dh_final, dq, dk, dv, dh0, workspace,
+                       workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- group norm
+namespace {
+
+dp_status make_gn(const dp_gn_dims *d, dp::GroupNorm *p)
+{
+    if (!d) return DP_ERR_INVALID_ARG;
+    if (d->N < 0 || d->S < 1 || d->C < 1 || d->G < 1 || d->C % d->G != 0) return DP_ERR_INVALID_ARG;
+    if (d->dtype != DP_F32 && d->dtype != DP_BF16) return DP_ERR_INVALID_ARG;
+    if (d->act != DP_ACT_NONE && d->act != DP_ACT_SILU) return DP_ERR_INVALID_ARG;
+    if (!(d->eps >= 0.f) || d->eps > 3.4e38f) return DP_ERR_INVALID_ARG;
+    // the grids are at most one CTA per (sample, group); rows fit an int
+    if ((long long)d->N * d->G > 0x7fffffffll || (long long)d->N * d->S > 0x7fffffffll) return DP_ERR_UNSUPPORTED;
+    memset(p, 0, sizeof(*p));
+    p->N = d->N; p->S = d->S; p->C = d->C; p->G = d->G;
+    p->dtype = d->dtype; p->act = d->act; p->eps = d->eps;
+    return DP_OK;
+}
+
+size_t gn_workspace(size_t scratch) { return kStatusBlock + ((scratch + 255) & ~(size_t)255); }
+
+}  // namespace
+
+extern "C" {
+
+dp_status dp_group_norm_workspace_size(const dp_gn_dims *dims, size_t *bytes)
+{
+    dp::GroupNorm p;
+    if (!bytes) return DP_ERR_INVALID_ARG;
+    DP_TRY(make_gn(dims, &p));
+    *bytes = gn_workspace(dp::gn_forward_scratch_bytes(p));
+    return DP_OK;
+}
+
+dp_status dp_group_norm_backward_workspace_size(const dp_gn_dims *dims, size_t *bytes)
+{
+    dp::GroupNorm p;
+    if (!bytes) return DP_ERR_INVALID_ARG;
+    DP_TRY(make_gn(dims, &p));
+    *bytes = gn_workspace(dp::gn_backward_scratch_bytes(p));
+    return DP_OK;
+}
+
+dp_status dp_group_norm(const dp_gn_dims *dims, const void *x, const void *weight, const void *bias, void *y,
+                        float *mean, float *rstd, void *workspace, size_t workspace_bytes, dp_stream_t stream)
+{
+    dp::GroupNorm p;
+    DP_TRY(make_gn(dims, &p));
+    if (p.N == 0) return DP_OK;
+    const size_t el = p.dtype == DP_F32 ? 4 : 2;
+    DP_TRY(check_ptr(x, 16));
+    DP_TRY(check_ptr(y, 16));
+    if (weight) DP_TRY(check_ptr(weight, el));
+    if (bias) DP_TRY(check_ptr(bias, el));
+    if (mean) DP_TRY(check_ptr(mean, 4));
+    if (rstd) DP_TRY(check_ptr(rstd, 4));
+    DP_TRY(check_workspace(workspace, workspace_bytes, gn_workspace(dp::gn_forward_scratch_bytes(p))));
+    p.x = x; p.weight = weight; p.bias = bias; p.y = y; p.mean = mean; p.rstd = rstd;
+    p.scratch = (float *)((char *)workspace + kStatusBlock);
+    p.stream = (cudaStream_t)stream;
+    return from_cuda(dp::launch_gn_forward(p));
+}
+
+dp_status dp_group_norm_backward(const dp_gn_dims *dims, const void *dy, const void *x, const void *weight,
+                                 const void *bias, const float *mean, const float *rstd, void *dx, float *dweight,
+                                 float *dbias, void *workspace, size_t workspace_bytes, dp_stream_t stream)
+{
+    dp::GroupNorm p;
+    DP_TRY(make_gn(dims, &p));
+    const size_t el = p.dtype == DP_F32 ? 4 : 2;
+    if (dweight) DP_TRY(check_ptr(dweight, 4));
+    if (dbias) DP_TRY(check_ptr(dbias, 4));
+    if (p.N > 0) {
+        DP_TRY(check_ptr(dy, 16));
+        DP_TRY(check_ptr(x, 16));
+        DP_TRY(check_ptr(dx, 16));
+        DP_TRY(check_ptr(mean, 4));
+        DP_TRY(check_ptr(rstd, 4));
+        if (weight) DP_TRY(check_ptr(weight, el));
+        if (bias) DP_TRY(check_ptr(bias, el));
+        DP_TRY(check_workspace(workspace, workspace_bytes, gn_workspace(dp::gn_backward_scratch_bytes(p))));
+    }
+    if (p.N == 0) {   // sums over no rows
+        for (float *t : {dweight, dbias})
+            if (t && cudaMemsetAsync(t, 0, p.C * sizeof(float), (cudaStream_t)stream) != cudaSuccess)
+                return DP_ERR_CUDA;
+        return DP_OK;
+    }
+    p.x = x; p.weight = weight; p.bias = bias; p.dy = dy; p.dx = dx;
+    p.mean = const_cast<float *>(mean); p.rstd = const_cast<float *>(rstd);
+    p.dweight = dweight; p.dbias = dbias;
+    p.scratch = (float *)((char *)workspace + kStatusBlock);
+    p.stream = (cudaStream_t)stream;
+    return from_cuda(dp::launch_gn_backward(p));
+}
+
+}  // extern "C"

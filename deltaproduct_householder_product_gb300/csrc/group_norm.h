@@ -1,0 +1,28 @@
+// Group norm, channels last: one validated problem (dp_group_norm,
+// dp_group_norm_backward; layouts in dp.h).
+#pragma once
+
+#include "internal.h"
+
+namespace dp {
+
+struct GroupNorm {
+    long long N;
+    int S, C, G;
+    int dtype;                    // dp_dtype of x, y, dy, dx, weight, bias
+    int act;                      // dp_act
+    float eps;
+    const void *x, *weight, *bias, *dy;
+    void *y, *dx;
+    float *mean, *rstd;           // [N,G]: written forward, read backward
+    float *dweight, *dbias;       // [C]
+    float *scratch;
+    cudaStream_t stream;
+};
+
+size_t gn_forward_scratch_bytes(const GroupNorm &p);
+cudaError_t launch_gn_forward(const GroupNorm &p);
+size_t gn_backward_scratch_bytes(const GroupNorm &p);
+cudaError_t launch_gn_backward(const GroupNorm &p);
+
+}  // namespace dp

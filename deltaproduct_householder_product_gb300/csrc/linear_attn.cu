@@ -1,0 +1,390 @@
+// Linear attention with a decay for each head, on CUDA cores in fp32: the
+// chunked pass for any supported size and type, and the one-token step.
+// linear_attn.h states the recurrence and its chunked form.
+#include "linear_attn.h"
+
+namespace dp {
+namespace {
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f(float *p, float x) { *p = x; }
+__device__ __forceinline__ void from_f(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+
+// 16 bytes of T as floats
+template <typename T> struct Vec16;
+template <> struct Vec16<float> {
+    static constexpr int n = 4;
+    static __device__ __forceinline__ void load(const float *p, float (&f)[4])
+    {
+        const float4 v = *(const float4 *)p;
+        f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    }
+};
+template <> struct Vec16<__nv_bfloat16> {
+    static constexpr int n = 8;
+    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&f)[8])
+    {
+        const uint4 v = *(const uint4 *)p;
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+
+constexpr int kC = 32;          // rows of a chunk
+constexpr int kThreads = 256;
+
+template <int DX, int DZ> struct Tile {
+    static constexpr int LX = DX + 4, LZ = DZ + 4;        // padded rows: 16-byte aligned, conflict-free column walks
+    static constexpr int NX = DX / 16, NZ = DZ / 16;      // state block of a thread
+    static constexpr int RO = DZ / 32;                    // output rows of a thread (4 columns each)
+    static constexpr size_t bytes = sizeof(float) * (2 * kC * LX + kC * LZ + DX * LZ + kC * (kC + 1) + 2 * (kC + 1) + 4);
+};
+
+// [kC][D] rows of the sequence into padded fp32 rows; rows that are not
+// live hold zeros (whatever the neighbouring memory holds is never read)
+template <int D, typename T>
+__device__ __forceinline__ void load_rows(float *dst, const T *src, size_t row, int H, int h, int live)
+{
+    constexpr int n = Vec16<T>::n, per = D / n;
+    for (int i = threadIdx.x; i < kC * per; i += kThreads) {
+        const int r = i / per, c = (i - r * per) * n;
+        float f[n] = {};
+        if (r < live) Vec16<T>::load(src + ((row + r) * H + h) * D + c, f);
+#pragma unroll
+        for (int j = 0; j < n; j += 4)
+            *(float4 *)(dst + r * (D + 4) + c + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+    }
+}
+
+// One CTA runs one segment of one (sequence, head) with the whole state in
+// registers (a 16 x 16 grid of threads, DX/16 x DZ/16 blocks) and a copy of
+// it in shared memory for the readout. With P > 1 the CTAs of a cluster hold
+// the sequence's segments: each first sums its own rows into a state from
+// zero, they exchange those through global memory, and each then starts from
+// the decayed sum of the segments before it.
+template <int DX, int DZ, typename T>
+__global__ void __launch_bounds__(kThreads)
+la_simt_kernel(LaPass p)
+{
+    using L = Tile<DX, DZ>;
+    extern __shared__ float sm[];
+    float *X = sm, *Y = X + kC * L::LX, *Z = Y + kC * L::LX, *S = Z + kC * L::LZ, *A = S + DX * L::LZ;
+    float *pw = A + kC * (kC + 1);                // gamma^0 .. gamma^kC
+    float2 *pc = (float2 *)(pw + ((kC + 2) & ~1));   // gamma^kC, gamma^R of the ragged chunk
+
+    const LaSegment g = la_segment(p.cu, p.N, p.T, p.H, p.max_T, p.P, kC, blockIdx.x);
+    if (!g.ok) {   // the whole cluster sees the same offsets and leaves together
+        if (threadIdx.x == 0 && g.h == 0 && g.rank == 0) report_bad_sequence(p.status);
+        return;
+    }
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const float ld = p.log_decay[g.h];
+    const int ragged = g.len % kC;
+    if (tid <= kC) pw[tid] = la_power(ld, tid);
+    if (tid == 64) pc[0] = la_power2(ld, kC);
+    if (tid == 96) pc[1] = la_power2(ld, ragged);
+    __syncthreads();
+
+    const size_t cells = (size_t)DX * DZ, head = (size_t)g.n * p.H + g.h;
+    const int rev = p.reverse ? 1 : 0;
+    float s[L::NX][L::NZ];
+    const auto init_at = [&](int a, int b) -> size_t {
+        const int r = ty * L::NX + a, c = tx * L::NZ + b;
+        return head * cells + (p.state_t ? (size_t)c * DX + r : (size_t)r * DZ + c);
+    };
+    const int chunks = (g.end - g.begin + kC - 1) / kC;
+
+    // S <- gamma^R S + sum_r weight_r y_r z_r^T over the loaded chunk
+    const auto update = [&](int live) {
+        const float2 wc = live == kC ? pc[0] : pc[1];
+#pragma unroll
+        for (int a = 0; a < L::NX; ++a)
+#pragma unroll
+            for (int b = 0; b < L::NZ; ++b) s[a][b] = fmaf(s[a][b], wc.x, s[a][b] * wc.y);
+        for (int r = 0; r < live; ++r) {
+            const float w = pw[rev ? r + 1 : live - 1 - r];
+            float yv[L::NX], zv[L::NZ];
+#pragma unroll
+            for (int a = 0; a < L::NX; ++a) yv[a] = w * Y[r * L::LX + ty * L::NX + a];
+#pragma unroll
+            for (int b = 0; b < L::NZ; ++b) zv[b] = Z[r * L::LZ + tx * L::NZ + b];
+#pragma unroll
+            for (int a = 0; a < L::NX; ++a)
+#pragma unroll
+                for (int b = 0; b < L::NZ; ++b) s[a][b] = fmaf(yv[a], zv[b], s[a][b]);
+        }
+    };
+
+#pragma unroll
+    for (int a = 0; a < L::NX; ++a)
+#pragma unroll
+        for (int b = 0; b < L::NZ; ++b) s[a][b] = 0.f;
+
+    const int last_rank = g.len > 0 ? (g.len - 1) / g.seg : 0;
+    if (p.P > 1) {
+        // the segment's own state, for the segments that follow it
+        const bool needed = chunks > 0 && (rev ? g.rank > 0 : g.rank < last_rank);
+        if (needed) {
+            for (int i = 0; i < chunks; ++i) {
+                const int c = rev ? chunks - 1 - i : i, row = g.begin + c * kC;
+                const int live = g.end - row < kC ? g.end - row : kC;
+                load_rows<DX, T>(Y, (const T *)p.y, g.row0 + row, p.H, g.h, live);
+                load_rows<DZ, T>(Z, (const T *)p.z, g.row0 + row, p.H, g.h, live);
+                __syncthreads();
+                update(live);
+                __syncthreads();
+            }
+            float *dst = p.part + (head * p.P + g.rank) * cells;
+#pragma unroll
+            for (int a = 0; a < L::NX; ++a)
+#pragma unroll
+                for (int b = 0; b < L::NZ; ++b) dst[(ty * L::NX + a) * DZ + tx * L::NZ + b] = s[a][b];
+        }
+        __threadfence();
+        cluster_arrive();
+        cluster_wait();
+    }
+
+    // the state entering the segment
+    {
+        const float w0 = la_power(ld, rev ? g.len - g.end : g.begin);
+#pragma unroll
+        for (int a = 0; a < L::NX; ++a)
+#pragma unroll
+            for (int b = 0; b < L::NZ; ++b)
+                s[a][b] = p.init ? w0 * p.init[init_at(a, b)] : 0.f;
+        const int from = rev ? g.rank + 1 : 0, to = rev ? last_rank + 1 : (g.rank <= last_rank ? g.rank : 0);
+        for (int q = from; q < to; ++q) {
+            const int gap = rev ? q * g.seg - g.end : g.begin - (q + 1) * g.seg;
+            const float w = la_power(ld, gap);
+            const float *src = p.part + (head * p.P + q) * cells;
+#pragma unroll
+            for (int a = 0; a < L::NX; ++a)
+#pragma unroll
+                for (int b = 0; b < L::NZ; ++b)
+                    s[a][b] = fmaf(w, __ldcg(src + (ty * L::NX + a) * DZ + tx * L::NZ + b), s[a][b]);
+        }
+    }
+
+    for (int i = 0; i < chunks; ++i) {
+        const int c = rev ? chunks - 1 - i : i, row = g.begin + c * kC;
+        const int live = g.end - row < kC ? g.end - row : kC;
+#pragma unroll
+        for (int a = 0; a < L::NX; ++a)
+#pragma unroll
+            for (int b = 0; b < L::NZ; ++b) S[(ty * L::NX + a) * L::LZ + tx * L::NZ + b] = s[a][b];
+        load_rows<DX, T>(X, (const T *)p.x, g.row0 + row, p.H, g.h, live);
+        load_rows<DX, T>(Y, (const T *)p.y, g.row0 + row, p.H, g.h, live);
+        load_rows<DZ, T>(Z, (const T *)p.z, g.row0 + row, p.H, g.h, live);
+        __syncthreads();
+        {   // A[r][s] = gamma^|r-s| x_r . y_s on the seen side, 0 elsewhere
+            const int r = tid >> 3, s0 = tid & 7;
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+            for (int d = 0; d < DX; d += 4) {
+                const float4 xv = *(const float4 *)(X + r * L::LX + d);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 yv = *(const float4 *)(Y + (s0 + 8 * j) * L::LX + d);
+                    acc[j] = fmaf(xv.x, yv.x, fmaf(xv.y, yv.y, fmaf(xv.z, yv.z, fmaf(xv.w, yv.w, acc[j]))));
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int q = s0 + 8 * j, far = rev ? q - r : r - q;
+                A[r * (kC + 1) + q] = far >= 0 && q < live ? pw[far] * acc[j] : 0.f;
+            }
+        }
+        __syncthreads();
+        {   // out_r = gamma^(r'+o) S^T x_r + sum_s A[r][s] z_s
+            constexpr int per = DZ / 4;
+            const int col = (tid % per) * 4, r0 = (tid / per) * L::RO;
+            float acc[L::RO][4];
+#pragma unroll
+            for (int a = 0; a < L::RO; ++a)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) acc[a][b] = 0.f;
+#pragma unroll 4
+            for (int d = 0; d < DX; d += 4) {
+                float4 xv[L::RO];
+#pragma unroll
+                for (int a = 0; a < L::RO; ++a) xv[a] = *(const float4 *)(X + (r0 + a) * L::LX + d);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 sv = *(const float4 *)(S + (d + j) * L::LZ + col);
+#pragma unroll
+                    for (int a = 0; a < L::RO; ++a) {
+                        const float xx = j == 0 ? xv[a].x : j == 1 ? xv[a].y : j == 2 ? xv[a].z : xv[a].w;
+                        acc[a][0] = fmaf(xx, sv.x, acc[a][0]);
+                        acc[a][1] = fmaf(xx, sv.y, acc[a][1]);
+                        acc[a][2] = fmaf(xx, sv.z, acc[a][2]);
+                        acc[a][3] = fmaf(xx, sv.w, acc[a][3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < L::RO; ++a) {
+                const int r = r0 + a;
+                const float w = r < live ? pw[rev ? live - 1 - r : r + 1] : 0.f;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) acc[a][b] *= w;
+            }
+            for (int q = 0; q < live; ++q) {
+                const float4 zv = *(const float4 *)(Z + q * L::LZ + col);
+#pragma unroll
+                for (int a = 0; a < L::RO; ++a) {
+                    const float w = A[(r0 + a) * (kC + 1) + q];
+                    acc[a][0] = fmaf(w, zv.x, acc[a][0]);
+                    acc[a][1] = fmaf(w, zv.y, acc[a][1]);
+                    acc[a][2] = fmaf(w, zv.z, acc[a][2]);
+                    acc[a][3] = fmaf(w, zv.w, acc[a][3]);
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < L::RO; ++a)
+                if (r0 + a < live) {
+                    T *dst = (T *)p.out + ((g.row0 + row + r0 + a) * p.H + g.h) * DZ + col;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) from_f(dst + b, acc[a][b]);
+                }
+        }
+        update(live);
+        __syncthreads();
+    }
+    if (p.fin && g.rank == (rev ? 0 : last_rank))
+#pragma unroll
+        for (int a = 0; a < L::NX; ++a)
+#pragma unroll
+            for (int b = 0; b < L::NZ; ++b) p.fin[init_at(a, b)] = s[a][b];
+}
+
+template <int DX, int DZ, typename T>
+cudaError_t launch_sized(const LaPass &p)
+{
+    auto kernel = la_simt_kernel<DX, DZ, T>;
+    constexpr size_t smem = Tile<DX, DZ>::bytes + 64;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((size_t)p.N * p.H * p.P));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = p.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.P;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <typename T>
+cudaError_t launch_typed(const LaPass &p)
+{
+    switch (p.Dx * 1000 + p.Dz) {
+    case 32032: return launch_sized<32, 32, T>(p);
+    case 32064: return launch_sized<32, 64, T>(p);
+    case 32128: return launch_sized<32, 128, T>(p);
+    case 64032: return launch_sized<64, 32, T>(p);
+    case 64064: return launch_sized<64, 64, T>(p);
+    case 64128: return launch_sized<64, 128, T>(p);
+    case 128032: return launch_sized<128, 32, T>(p);
+    case 128064: return launch_sized<128, 64, T>(p);
+    default: return launch_sized<128, 128, T>(p);
+    }
+}
+
+// ---------------------------------------------------------------- one token
+// A thread owns 4 columns of the state and every kStepRows-th row of them:
+// 16 bytes of state per load and store, one pass over it. The rows' partial
+// outputs are added across the threads of a column group in shared memory.
+constexpr int kStepThreads = 128;
+
+template <int DK, typename T>
+__global__ void __launch_bounds__(kStepThreads)
+la_step_kernel(int H, int Dv, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+               const float *__restrict__ log_decay, float *state, T *__restrict__ o)
+{
+    constexpr int kCols = 32, kGroups = kCols / 4, kStepRows = kStepThreads / kGroups;
+    __shared__ float4 part[kStepRows][kGroups];
+    const int bh = blockIdx.x, cg = threadIdx.x % kGroups, rg = threadIdx.x / kGroups;
+    const int col = blockIdx.y * kCols + cg * 4;
+    float4 *S = (float4 *)(state + (size_t)bh * DK * Dv + col);
+    const int ld4 = Dv / 4;
+    float4 s[DK / kStepRows];
+#pragma unroll
+    for (int i = 0; i < DK / kStepRows; ++i) s[i] = S[(size_t)(rg + i * kStepRows) * ld4];
+    const float g = la_power(log_decay[bh % H], 1);
+    float vv[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) vv[j] = to_f(v[(size_t)bh * Dv + col + j]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < DK / kStepRows; ++i) {
+        const int r = rg + i * kStepRows;
+        const float kk = to_f(k[(size_t)bh * DK + r]), qq = to_f(q[(size_t)bh * DK + r]);
+        s[i].x = fmaf(g, s[i].x, kk * vv[0]);
+        s[i].y = fmaf(g, s[i].y, kk * vv[1]);
+        s[i].z = fmaf(g, s[i].z, kk * vv[2]);
+        s[i].w = fmaf(g, s[i].w, kk * vv[3]);
+        S[(size_t)r * ld4] = s[i];
+        acc.x = fmaf(qq, s[i].x, acc.x);
+        acc.y = fmaf(qq, s[i].y, acc.y);
+        acc.z = fmaf(qq, s[i].z, acc.z);
+        acc.w = fmaf(qq, s[i].w, acc.w);
+    }
+    part[rg][cg] = acc;
+    __syncthreads();
+    if (threadIdx.x < kCols) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kStepRows; ++i) sum += ((const float *)&part[i][0])[threadIdx.x];
+        from_f(o + (size_t)bh * Dv + blockIdx.y * kCols + threadIdx.x, sum);
+    }
+}
+
+template <int DK, typename T>
+cudaError_t launch_step_sized(const LaStep &p)
+{
+    la_step_kernel<DK, T><<<dim3(p.B * p.H, p.Dv / 32), kStepThreads, 0, p.stream>>>(
+        p.H, p.Dv, (const T *)p.q, (const T *)p.k, (const T *)p.v, p.log_decay, p.state, (T *)p.o);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_step_typed(const LaStep &p)
+{
+    return p.Dk == 32   ? launch_step_sized<32, T>(p)
+           : p.Dk == 64 ? launch_step_sized<64, T>(p)
+                        : launch_step_sized<128, T>(p);
+}
+
+}  // namespace
+
+// Segments of at least two chunks, and no more CTAs than SMs.
+int la_simt_cluster(int N, int H, int max_T)
+{
+    int P = 1;
+    while (P < kLaMaxCluster && (long long)N * H * P * 2 <= 152 && max_T >= 4 * P * kC) P *= 2;
+    return P;
+}
+
+cudaError_t launch_la_simt(const LaPass &p)
+{
+    if ((size_t)p.N * p.H == 0) return cudaSuccess;
+    return p.dtype == DP_F32 ? launch_typed<float>(p) : launch_typed<__nv_bfloat16>(p);
+}
+
+cudaError_t launch_la_step(const LaStep &p)
+{
+    if ((size_t)p.B * p.H == 0) return cudaSuccess;
+    return p.dtype == DP_F32 ? launch_step_typed<float>(p) : launch_step_typed<__nv_bfloat16>(p);
+}
+
+}  // namespace dp

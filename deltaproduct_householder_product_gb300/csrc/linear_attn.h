@@ -1,0 +1,111 @@
+// Linear attention with a decay for each head: declarations shared by its
+// translation units.
+//
+// Everything the operator computes is one recurrence over a sequence's rows,
+// a "pass" (gamma = exp(log_decay[h])):
+//   forward   S_t = gamma S_{t-1} + y_t z_t^T         out_t = S_t^T x_t
+//   reverse   G_t = y_t z_t^T + gamma G_{t+1}         out_t = G_t^T x_t
+// with S_{-1} = init, and gamma G_T := init (a gradient that reaches the
+// final state reaches the last token undecayed). `fin` is S_{T-1}, or
+// gamma G_0. The outputs are x, y, z = q, k, v forward; the gradients are
+//   dq: d_o, v, k forward from h0^T;  dv: k, q, d_o reverse from dh_final
+//   (fin: dh0);  dk: v, d_o, q reverse from dh_final^T.
+//
+// In chunks of C rows, with E the state entering the chunk and r' = r
+// forward, C-1-r reverse:
+//   out_r = sum_{s on the seen side} gamma^|r-s| (x_r . y_s) z_s
+//           + gamma^(r' + o) E^T x_r                       o = 1 forward, 0 reverse
+//   E_next = gamma^R E + sum_r gamma^(R-1-r' + 1-o) y_r z_r^T   (R live rows)
+#pragma once
+
+#include "internal.h"
+
+namespace dp {
+
+struct LaPass {
+    int N, T, H;               // sequences, rows of the time axis, heads
+    int Dx, Dz;                // state rows (x, y) and columns (z, out)
+    int dtype;                 // dp_dtype of x, y, z, out
+    const void *x, *y, *z;
+    void *out;
+    const float *log_decay;    // [H]
+    const float *init;         // [N,H,Dx,Dz], or [N,H,Dz,Dx] with state_t; NULL: zeros
+    float *fin;                // as init; NULL: not written
+    bool state_t;              // init and fin hold the transposed state
+    bool reverse;
+    const int *cu;             // packed sequences (NULL: dense)
+    int max_T;                 // longest sequence
+    int P;                     // CTAs (one cluster) per sequence and head
+    float *part;               // [N,H,P,Dx,Dz] states of the segments (P > 1)
+    uint32_t *status;
+    cudaStream_t stream;
+};
+
+constexpr int kLaMaxCluster = 8;
+
+// CUDA-core kernel: any supported size and type, fp32 arithmetic.
+int la_simt_cluster(int N, int H, int max_T);
+cudaError_t launch_la_simt(const LaPass &p);
+
+// One token: state <- gamma state + k v^T, o = state^T q.
+struct LaStep {
+    int B, H, Dk, Dv, dtype;
+    const void *q, *k, *v;
+    const float *log_decay;
+    float *state;
+    void *o;
+    cudaStream_t stream;
+};
+cudaError_t launch_la_step(const LaStep &p);
+
+// ---- the part of a sequence that one CTA of a cluster runs: rows
+// [begin, end) of the sequence, in segments of whole chunks
+struct LaSegment {
+    int n, h;            // sequence, head
+    int rank;            // segment of the sequence
+    size_t row0;         // first row of the sequence in the [rows, H, D] layout
+    int len, seg;        // rows of the sequence, of a segment
+    int begin, end;
+    bool ok;
+};
+
+__device__ __forceinline__ LaSegment la_segment(const int *cu, int N, int T, int H, int max_T, int P, int chunk,
+                                                unsigned block)
+{
+    LaSegment g;
+    const unsigned nh = block / P;
+    g.rank = (int)(block - nh * P);
+    g.n = (int)(nh / H);
+    g.h = (int)(nh - (unsigned)g.n * H);
+    const SeqRange sq = seq_range(cu, g.n, N, T, max_T);
+    g.ok = sq.ok;
+    g.row0 = (size_t)sq.b_map * T + sq.t0;
+    g.len = sq.len;
+    const int chunks = (g.len + chunk - 1) / chunk;
+    g.seg = (chunks + P - 1) / P * chunk;
+    g.begin = g.rank * g.seg < g.len ? g.rank * g.seg : g.len;
+    g.end = g.begin + g.seg < g.len ? g.begin + g.seg : g.len;
+    return g;
+}
+
+// gamma^n for a log decay; n = 0 gives 1 for every decay (a decay of 0 included).
+__device__ __forceinline__ float la_power(float log_decay, int n)
+{
+    return n == 0 ? 1.f : expf((float)n * log_decay);
+}
+
+// gamma^n as the sum of two fp32 values. The state is multiplied by the same
+// power once per chunk, so a rounding of that power would grow with the
+// number of chunks a head remembers.
+__device__ __forceinline__ float2 la_power2(float log_decay, int n)
+{
+    if (n == 0) return make_float2(1.f, 0.f);
+    const double w = exp((double)n * (double)log_decay);
+    const float hi = (float)w;
+    return make_float2(hi, isfinite(hi) ? (float)(w - (double)hi) : 0.f);
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+}  // namespace dp

@@ -96,7 +96,7 @@ typedef enum {
 } dp_prologue_flags;
 
 /* ABI version of this header (bumped on any signature change). */
-#define DP_ABI_VERSION 10
+#define DP_ABI_VERSION 11
 int dp_abi_version(void);
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -300,6 +300,111 @@ dp_status dp_forward_write_keys(const dp_dims *dims, const void *q, const void *
                                 const void *v, const void *beta, const void *g, const float *h0,
                                 void *o, float *h_final, void *workspace, size_t workspace_bytes,
                                 dp_stream_t stream);
+
+/* Linear attention with a decay for each head (the plain decayed sum of
+ * outer products, a library facility beside the delta-update recurrence: the
+ * same state layout and readout, no error term). Per batch b, head h, with
+ * gamma = exp(log_decay[h]) and the D_k x D_v matrix state S:
+ *
+ *     S_t = gamma S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t
+ *
+ * Layouts are contiguous row-major: q, k [B,T,H,D_k], v, o [B,T,H,D_v] of
+ * type dims->dtype (o is rounded once, from fp32); log_decay [H] fp32, a
+ * constant of the head (it has no gradient), meant to be <= 0 (-inf: a decay
+ * of 0, every token on its own); states [B,H,D_k,D_v] fp32. No scale is
+ * applied to the scores: scale q. Values are expected finite: a token's NaN
+ * or infinity may reach every output of the up to 128 tokens it is processed
+ * with, besides those that the recurrence carries it to, but never another
+ * sequence or head. Same error rules, stream and memory rules as above. */
+typedef struct {
+    int B, T, H;     /* batch, tokens, heads (T may be 0) */
+    int Dk, Dv;      /* key and value head dims: 32, 64 or 128 */
+    int dtype;       /* dp_dtype of q, k, v, o, d_o, dq, dk, dv */
+    int impl;        /* dp_impl: RECURRENT the CUDA-core kernel (any type),
+                        CHUNK_TC the tensor-core kernel (bf16), AUTO the
+                        tensor-core kernel for bf16 */
+    int max_seqlen;  /* varlen calls: the longest packed sequence; else 0 */
+} dp_la_dims;
+
+/* Bytes of device workspace of the calls below (>= 256; the status block,
+ * then the states of the segments that a sequence is cut into where few
+ * sequences and heads would leave SMs idle). It depends on dims and on the
+ * current device. Calls sharing a workspace must be ordered (one stream);
+ * contents need not be kept between calls, except for the status word. */
+dp_status dp_linear_attention_workspace_size(const dp_la_dims *dims, size_t *bytes);
+dp_status dp_linear_attention_backward_workspace_size(const dp_la_dims *dims, size_t *bytes);
+
+/* Whole sequences. h0: initial state, NULL = zeros; h_final: final state,
+ * NULL = not written, may alias h0. T = 0 copies h0 (or zeros) to h_final. */
+dp_status dp_linear_attention(const dp_la_dims *dims, const void *q, const void *k, const void *v,
+                              const float *log_decay, const float *h0, void *o, float *h_final,
+                              void *workspace, size_t workspace_bytes, dp_stream_t stream);
+/* Packed sequences: dims->B = N sequences, dims->T = total tokens,
+ * cu_seqlens and the layouts as in dp_forward_varlen (offsets that break its
+ * rules record DP_ERR_DEVICE and nothing of that sequence is computed). */
+dp_status dp_linear_attention_varlen(const dp_la_dims *dims, const int *cu_seqlens, const void *q,
+                                     const void *k, const void *v, const float *log_decay,
+                                     const float *h0, void *o, float *h_final, void *workspace,
+                                     size_t workspace_bytes, dp_stream_t stream);
+
+/* One token on a carried state, updated in place (dims->T is ignored):
+ * q, k [B,H,D_k], v, o [B,H,D_v], state [B,H,D_k,D_v] fp32. */
+dp_status dp_linear_attention_step(const dp_la_dims *dims, const void *q, const void *k, const void *v,
+                                   const float *log_decay, float *state, void *o, dp_stream_t stream);
+
+/* Gradients of L = <d_o, o> + <dh_final, h_final> with respect to q, k, v
+ * and h0. With G_t the gradient of S_t through o_t and later tokens,
+ * G_t = q_t d_o_t^T + gamma G_{t+1} (gamma G_T := dh_final):
+ *     dq_t = S_t d_o_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,  dh0 = gamma G_0.
+ * d_o [B,T,H,D_v], dq, dk, dv of type dims->dtype in the layouts of q, k, v
+ * (each rounded once, from fp32; all written in full); dh_final fp32 or NULL
+ * (zeros); dh0 fp32 or NULL (not written), may alias dh_final. No atomics:
+ * the results are deterministic. */
+dp_status dp_linear_attention_backward(const dp_la_dims *dims, const void *q, const void *k,
+                                       const void *v, const float *log_decay, const float *h0,
+                                       const void *d_o, const float *dh_final, void *dq, void *dk,
+                                       void *dv, float *dh0, void *workspace, size_t workspace_bytes,
+                                       dp_stream_t stream);
+dp_status dp_linear_attention_backward_varlen(const dp_la_dims *dims, const int *cu_seqlens,
+                                              const void *q, const void *k, const void *v,
+                                              const float *log_decay, const float *h0, const void *d_o,
+                                              const float *dh_final, void *dq, void *dk, void *dv,
+                                              float *dh0, void *workspace, size_t workspace_bytes,
+                                              dp_stream_t stream);
+
+/* Group norm with an activation, channels last: x, y [N,S,C], G groups of
+ * C / G neighbouring channels; the statistics of (n, g) run over the S
+ * positions and the group's channels (S = 1: over the group's channels of
+ * each row, the norm of each head's output when x is o [B,T,H,D_v] with
+ * N = B T, C = H D_v, G = H):
+ *     z = (x - mean) rstd w + b,  rstd = (var + eps)^-1/2,  y = act(z)
+ * with the biased variance, fp32 arithmetic. weight, bias [C] of type
+ * dims->dtype or NULL (1, 0); mean, rstd [N,G] fp32 outputs or NULL. y may
+ * alias x. */
+typedef enum { DP_ACT_NONE = 0, DP_ACT_SILU = 1 } dp_act;
+typedef struct {
+    int N, S, C;     /* samples (may be 0), positions, channels */
+    int G;           /* groups; divides C */
+    int dtype;       /* dp_dtype of x, y, dy, dx, weight, bias */
+    int act;         /* dp_act */
+    float eps;       /* >= 0 */
+} dp_gn_dims;
+dp_status dp_group_norm_workspace_size(const dp_gn_dims *dims, size_t *bytes);
+dp_status dp_group_norm(const dp_gn_dims *dims, const void *x, const void *weight, const void *bias,
+                        void *y, float *mean, float *rstd, void *workspace, size_t workspace_bytes,
+                        dp_stream_t stream);
+/* Its gradients, from the mean and rstd that dp_group_norm wrote:
+ *     h = (x - mean) rstd, d = dy act'(z), u = d w,
+ *     dx = rstd (u - E[u] - h E[u h]),  dweight = sum d h,  dbias = sum d
+ * (E over the values of (n, g)). dx [N,S,C] in dims->dtype, may alias dy;
+ * dweight, dbias [C] fp32, either may be NULL (not written); given for a
+ * NULL weight or bias they are the gradients at 1 and 0. No atomics: the
+ * results are deterministic. */
+dp_status dp_group_norm_backward_workspace_size(const dp_gn_dims *dims, size_t *bytes);
+dp_status dp_group_norm_backward(const dp_gn_dims *dims, const void *dy, const void *x, const void *weight,
+                                 const void *bias, const float *mean, const float *rstd, void *dx,
+                                 float *dweight, float *dbias, void *workspace, size_t workspace_bytes,
+                                 dp_stream_t stream);
 
 /* Synchronises `stream`, returns the status the device recorded in the
  * workspace since it was last cleared, and clears it. */

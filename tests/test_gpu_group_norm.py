@@ -1,0 +1,182 @@
+"""GPU parity of group norm with an activation and of its gradients against the
+fp64 oracle.
+
+Bounds: an fp32 sum of M terms is off by at most M 2^-24 of the sum of their
+sizes, far less in a tree; the statistics are held to 2^-18 of the values'
+spread (64 roundings) plus that share of the mean, outputs to 2^-16 (fp32) of
+1 + |value|, plus 2^-8 of the value where it is rounded to bf16."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import group_norm as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dp():
+    from deltaproduct_householder_product_gb300 import build
+    build.build()
+    import deltaproduct_householder_product_gb300 as dp
+    assert torch.cuda.is_available()
+    return dp
+
+
+# N, S, C, groups: heads of 128, odd widths, one value per group, one group,
+# groups that straddle 16-byte pieces, many rows, many positions
+SHAPES = [(1, 1, 8, 1), (3, 1, 1024, 8), (1000, 1, 256, 2), (7, 1, 99, 3), (5, 1, 4096, 1), (2, 1, 5000, 2),
+          (4, 1, 64, 64), (513, 1, 320, 32), (2, 7, 20, 2), (3, 129, 40, 4), (1, 1000, 96, 32), (2, 300, 330, 10),
+          (2, 2049, 640, 32), (1, 5000, 33, 1), (17, 3, 512, 2), (1, 20000, 64, 4)]
+
+
+def draw(N, S, C, dtype, seed, affine=True, shift=0.5):
+    g = torch.Generator().manual_seed(seed)
+
+    def rn(*s):
+        return torch.randn(*s, generator=g)
+
+    return ((1.5 * rn(N, S, C) + shift * rn(N, 1, 1)).to(dtype), (1 + 0.2 * rn(C)).to(dtype) if affine else None,
+            (0.2 * rn(C)).to(dtype) if affine else None, rn(N, S, C).to(dtype))
+
+
+def cuda(*ts):
+    return [None if t is None else t.cuda() for t in ts]
+
+
+def near(got, want, dtype, what, scale=1.0):
+    got = got.detach().cpu().double().numpy()
+    assert got.shape == want.shape and np.isfinite(got).all(), what
+    bound = scale * 2.0 ** -16 * (1 + np.abs(want)) + (2.0 ** -8 * np.abs(want) if dtype == torch.bfloat16 else 0)
+    err = np.abs(got - want)
+    assert (err <= bound).all(), (what, float((err / bound).max()))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N,S,C,G", SHAPES, ids=str)
+def test_forward_and_backward(dp, N, S, C, G, dtype):
+    for act, affine in (("silu", True), ("none", True), ("silu", False), ("none", False)):
+        x, w, b, dy = draw(N, S, C, dtype, N + S + C, affine)
+        xc, wc, bc, dyc = cuda(x, w, b, dy)
+        y, mean, rstd = dp.group_norm(xc, wc, bc, groups=G, act=act)
+        ry, rm, rr = ref.forward(x, w, b, G, 1e-5, act)
+        spread = 1 / rr
+        assert (np.abs(mean.cpu().double().numpy() - rm) <= 2.0 ** -18 * (spread + np.abs(rm))).all()
+        # a relative error of the spread; groups of one value have none
+        assert (np.abs(rstd.cpu().double().numpy() / rr - 1) <= 2.0 ** -16).all()
+        # a mean that is off by e moves z by e rstd: at most 2^-18 (1 + |mean| rstd)
+        near(y, ry, dtype, ("y", act, affine), scale=1 + float(np.abs(rm * rr).max()))
+        g = dp.group_norm_backward(dyc, xc, wc, bc, mean, rstd, groups=G, act=act)
+        rdx, rdw, rdb = ref.backward(dy, x, w, b, mean, rstd, G, act)
+        # dx is rstd times differences of terms of size |u| <= 8
+        near(g["dx"], rdx, dtype, ("dx", act, affine), scale=8 * float(rr.max()) * (1 + float(np.abs(rm * rr).max())))
+        if affine:
+            # sums of N S terms of either sign
+            s = 8 * np.sqrt(N * S) * (1 + float(np.abs(rm * rr).max()))
+            near(g["dweight"], rdw, torch.float32, "dweight", scale=s)
+            near(g["dbias"], rdb, torch.float32, "dbias", scale=s)
+        else:
+            assert g["dweight"] is None and g["dbias"] is None
+
+
+@pytest.mark.parametrize("N,S,C,G", [(64, 1, 512, 4), (2, 3000, 64, 4), (3, 50, 96, 4)], ids=str)
+def test_mean_far_from_zero(dp, N, S, C, G):
+    """A mean of 1000 spreads: squares are taken around the mean, so the
+    spread keeps its digits (the inputs' own rounding is in them exactly)."""
+    x, w, b, _ = draw(N, S, C, torch.float32, 3)
+    x = x + 1500.0
+    y, mean, rstd = dp.group_norm(*cuda(x, w, b), groups=G, act="silu")
+    ry, rm, rr = ref.forward(x, w, b, G, 1e-5, "silu")
+    assert (np.abs(mean.cpu().double().numpy() / rm - 1) <= 2.0 ** -20).all()
+    assert (np.abs(rstd.cpu().double().numpy() / rr - 1) <= 2.0 ** -12).all()
+
+
+def test_constant_groups(dp):
+    """No spread at all: rstd is eps^-1/2 and y is act(bias), in every path."""
+    for N, S, C, G in ((4, 1, 256, 2), (2, 100, 32, 2), (1, 4000, 64, 2), (3, 1, 66, 2)):
+        x = torch.full((N, S, C), 3.0, device="cuda")
+        b = torch.linspace(-1, 1, C, device="cuda")
+        y, mean, rstd = dp.group_norm(x, None, b, groups=G, eps=1e-2, act="none")
+        assert torch.equal(mean, torch.full_like(mean, 3.0))
+        assert (rstd - 10).abs().max() <= 1e-5
+        assert torch.equal(y, b.expand_as(y))
+
+
+@pytest.mark.parametrize("N,S,C,G", [(64, 1, 512, 4), (2, 3000, 64, 4), (3, 50, 99, 3)], ids=str)
+def test_in_place_repeats_and_neighbours(dp, N, S, C, G):
+    """y over x; the same bits every time; a NaN stays in its group."""
+    x, w, b, dy = draw(N, S, C, torch.bfloat16, 7)
+    x, w, b, dy = cuda(x, w, b, dy)
+    y, mean, rstd = dp.group_norm(x, w, b, groups=G, act="silu")
+    g = dp.group_norm_backward(dy, x, w, b, mean, rstd, groups=G, act="silu")
+    for _ in range(5):
+        y2, m2, r2 = dp.group_norm(x, w, b, groups=G, act="silu")
+        g2 = dp.group_norm_backward(dy, x, w, b, mean, rstd, groups=G, act="silu")
+        assert torch.equal(y, y2) and torch.equal(mean, m2) and torch.equal(rstd, r2)
+        assert all(torch.equal(g[n], g2[n]) for n in g)
+    z = x.clone()
+    dp.group_norm(z, w, b, groups=G, act="silu", out=z)
+    assert torch.equal(z, y)
+    z = x.clone()
+    z[1, S // 2, C // G] = float("nan")          # sample 1, group 1
+    y2 = dp.group_norm(z, w, b, groups=G, act="silu")[0]
+    W = C // G
+    assert y2[1, :, W:2 * W].isnan().all()
+    keep = torch.ones_like(y, dtype=torch.bool)
+    keep[1, :, W:2 * W] = False
+    assert torch.equal(y[keep], y2[keep])
+
+
+def test_backward_matches_differences(dp):
+    """Differences of the fp64 oracle's loss along a direction, against the
+    kernel's fp32 gradients: 1e-4 of the products' root sum."""
+    N, S, C, G = 3, 40, 48, 4
+    x, w, b, dy = draw(N, S, C, torch.float32, 9)
+    _, mean, rstd = dp.group_norm(*cuda(x, w, b), groups=G, act="silu")
+    g = dp.group_norm_backward(*cuda(dy, x, w, b), mean, rstd, groups=G, act="silu")
+    r = np.random.default_rng(2)
+    for name, at, grad in (("x", x, "dx"), ("w", w, "dweight"), ("b", b, "dbias")):
+        d = r.normal(size=tuple(at.shape))
+
+        def loss(e):
+            v = {"x": x.double().numpy(), "w": w.double().numpy(), "b": b.double().numpy()}
+            v[name] = v[name] + e * d
+            return (ref.forward(v["x"], v["w"], v["b"], G, 1e-5, "silu")[0] * dy.double().numpy()).sum()
+
+        want = (loss(1e-4) - loss(-1e-4)) / 2e-4
+        got = float((g[grad].cpu().double().numpy() * d).sum())
+        assert abs(got - want) <= 1e-4 * np.sqrt(N * S * C), (name, got, want)
+
+
+def test_views_empty_and_stream(dp):
+    """Middle axes are positions; no samples is a no-op with zero sums."""
+    x, w, b, dy = draw(2, 30, 64, torch.float32, 12)
+    xc, wc, bc, dyc = cuda(x, w, b, dy)
+    y = dp.group_norm(xc, wc, bc, groups=4)[0]
+    assert torch.equal(dp.group_norm(xc.view(2, 5, 6, 64), wc, bc, groups=4)[0].view_as(y), y)
+    e = torch.empty(0, 3, 64, device="cuda")
+    assert dp.group_norm(e, wc, bc, groups=4)[0].shape == e.shape
+    z = torch.empty(0, 4, device="cuda")
+    g = dp.group_norm_backward(e, e, wc, bc, z, z, groups=4)
+    assert not g["dweight"].any() and not g["dbias"].any()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y2 = dp.group_norm(xc, wc, bc, groups=4, stream=s)[0]
+    s.synchronize()
+    assert torch.equal(y, y2)
+
+
+def test_refusals(dp):
+    x = torch.zeros(2, 3, 64, device="cuda")
+    for bad, err in ((dict(groups=5), dp.DPError), (dict(groups=0), dp.DPError), (dict(eps=-1.0), dp.DPError),
+                     (dict(act="tanh"), ValueError), (dict(weight=torch.zeros(63, device="cuda")), ValueError),
+                     (dict(weight=torch.zeros(64, device="cuda").bfloat16()), TypeError),
+                     (dict(out=torch.zeros(2, 3, 32, device="cuda")), ValueError),
+                     (dict(workspace=torch.zeros(2, device="cuda")), dp.DPError)):
+        with pytest.raises(err):
+            dp.group_norm(x, **{"groups": 4, **bad})
+    with pytest.raises(ValueError):
+        dp.group_norm(x.transpose(0, 1), groups=4)
+    m = torch.zeros(2, 4, device="cuda")
+    with pytest.raises(ValueError):
+        dp.group_norm_backward(x, x, None, None, m[:, :2].contiguous(), m, groups=4)

@@ -1,0 +1,360 @@
+"""GPU parity of linear attention with a decay for each head (whole sequences,
+packed, one token, gradients) against the fp64 oracle.
+
+Bounds, from the arithmetic: fp32 results differ from the exact ones by at
+most (number of additions) 2^-23 of the recurrence of the absolute values
+(``oracle.linear_attention.magnitudes``), entry by entry, and by 4e-6 in RMS
+(additions in random order of sign: the square root of about 4096 terms in
+memory times 2^-24). bf16 outputs add the rounding of the result (2^-8 of it)
+and at most two roundings of intermediate values to bf16 (2^-8 of the terms
+each); in RMS a rounding costs at most 2^-8 / sqrt(3), two in quadrature stay
+below 2^-8."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import linear_attention as ref
+
+pytestmark = pytest.mark.gpu
+U32, U16 = 2.0 ** -23, 2.0 ** -8
+DECAYS = [-1 / 32, 0.0, -1 / 1024, -2.0, -float("inf"), -1 / 7]
+
+
+@pytest.fixture(scope="module")
+def dp():
+    from deltaproduct_householder_product_gb300 import build
+    build.build()
+    import deltaproduct_householder_product_gb300 as dp
+    assert torch.cuda.is_available()
+    return dp
+
+
+def draw(lead, Dk, Dv, dtype, seed, states, first=0):
+    """CPU tensors of a problem; heads take the decays in turn from ``first``."""
+    g = torch.Generator().manual_seed(seed)
+    H = lead[-1]
+
+    def unit(x):
+        return x / x.norm(dim=-1, keepdim=True)
+
+    def rn(*s):
+        return torch.randn(*s, generator=g)
+
+    return dict(q=unit(rn(*lead, Dk)).to(dtype), k=unit(torch.nn.functional.silu(rn(*lead, Dk))).to(dtype),
+                v=rn(*lead, Dv).to(dtype), log_decay=torch.tensor([DECAYS[(first + h) % 6] for h in range(H)]),
+                h0=rn(states, H, Dk, Dv), d_o=rn(*lead, Dv).to(dtype), dh=0.1 * rn(states, H, Dk, Dv))
+
+
+def np64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def check(got, want, size, n, dtype, what):
+    """``size``: the recurrence of absolute values, ``n``: additions per value."""
+    got = np64(got)
+    assert got.shape == want.shape, what
+    if want.size == 0:
+        return
+    bound = (n + 64) * U32 * size + 1e-30
+    rms = 4e-6
+    if dtype == torch.bfloat16:
+        bound = bound + U16 * (np.abs(want) + 2 * size)
+        rms = U16
+    err = np.abs(got - want)
+    assert np.isfinite(got).all(), what
+    assert (err <= bound).all(), (what, float((err / bound).max()))
+    scale = np.sqrt((want ** 2).mean())
+    assert np.sqrt((err ** 2).mean()) <= rms * max(scale, 1e-30), (what, float(np.sqrt((err ** 2).mean()) / scale))
+
+
+def sequences(x, lengths):
+    """Per-sequence views of a packed or dense problem: (rows, index)."""
+    if lengths is None:
+        return [({n: x[n][b] for n in ("q", "k", "v", "d_o")}, b) for b in range(x["q"].shape[0])]
+    cu = np.concatenate([[0], np.cumsum(lengths)])
+    return [({n: x[n][cu[b]:cu[b + 1]] for n in ("q", "k", "v", "d_o")}, b) for b in range(len(lengths))]
+
+
+def cu_of(lengths):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device="cuda")
+
+
+def check_forward(x, lengths, o, hf, use_h0=True):
+    dt = x["q"].dtype
+    for (rows, b), ob in zip(sequences(x, lengths),
+                             [o[b] for b in range(o.shape[0])] if lengths is None
+                             else torch.split(o, list(lengths))):
+        h0 = x["h0"][b] if use_h0 else None
+        a = (rows["q"], rows["k"], rows["v"], x["log_decay"], h0)
+        ro, rh = ref.forward(*a)
+        mo, mh = ref.magnitudes(*a)
+        n = ro.shape[0] + x["q"].shape[-1]
+        check(ob, ro, mo, n, dt, f"o of sequence {b}")
+        if hf is not None:
+            check(hf[b], rh, mh, n, torch.float32, f"h_final of sequence {b}")
+
+
+def check_backward(x, lengths, g, use_h0=True, use_dh=True):
+    dt = x["q"].dtype
+    parts = {n: ([g[n][b] for b in range(g[n].shape[0])] if lengths is None else torch.split(g[n], list(lengths)))
+             for n in ("dq", "dk", "dv")}
+    for rows, b in sequences(x, lengths):
+        h0, dh = (x["h0"][b] if use_h0 else None), (x["dh"][b] if use_dh else None)
+        a = (rows["q"], rows["k"], rows["v"], x["log_decay"], h0, rows["d_o"], dh)
+        want = ref.backward(*a)
+        size = ref.backward(*[None if t is None else t.float().abs() if i != 3 else t for i, t in enumerate(a)])
+        n = rows["q"].shape[0] + max(x["q"].shape[-1], x["v"].shape[-1])
+        for i, name in enumerate(("dq", "dk", "dv")):
+            check(parts[name][b], want[i], size[i], n, dt, f"{name} of sequence {b}")
+        check(g["dh0"][b], want[3], size[3], n, torch.float32, f"dh0 of sequence {b}")
+
+
+def impls(dp, dtype):
+    return ["recurrent", "auto"] if dtype == torch.bfloat16 else ["auto"]
+
+
+DENSE = [(1, 1, 1, 32, 32), (2, 5, 3, 64, 128), (1, 127, 2, 128, 128), (2, 128, 1, 128, 64), (1, 129, 3, 64, 64),
+         (1, 64, 2, 32, 32), (3, 33, 2, 32, 128), (1, 300, 2, 128, 32), (1, 1111, 2, 128, 128), (1, 2048, 1, 64, 64),
+         (40, 70, 5, 32, 64)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,T,H,Dk,Dv", DENSE, ids=str)
+def test_forward(dp, B, T, H, Dk, Dv, dtype):
+    x = draw((B, T, H), Dk, Dv, dtype, T + H, B, first=T)
+    c = {n: t.cuda() for n, t in x.items()}
+    for impl in impls(dp, dtype):
+        for h0 in (True, False):
+            ws = torch.zeros(dp.linear_attention_workspace_size(B, T, H, Dk, Dv, dtype=dtype, impl=impl),
+                             dtype=torch.uint8, device="cuda")
+            o, hf = dp.linear_attention(c["q"], c["k"], c["v"], c["log_decay"], c["h0"] if h0 else None, impl=impl,
+                                        workspace=ws)
+            dp.check_status(ws)
+            assert o.dtype == dtype and hf.dtype == torch.float32
+            check_forward(x, None, o, hf, h0)
+        o2, none = dp.linear_attention(c["q"], c["k"], c["v"], c["log_decay"], impl=impl, h_final=False)
+        assert none is None and torch.equal(o2, o)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,T,H,Dk,Dv", DENSE, ids=str)
+def test_backward(dp, B, T, H, Dk, Dv, dtype):
+    x = draw((B, T, H), Dk, Dv, dtype, T + H + 1, B, first=T)
+    c = {n: t.cuda() for n, t in x.items()}
+    for impl in impls(dp, dtype):
+        g = dp.linear_attention_backward(c["q"], c["k"], c["v"], c["log_decay"], c["h0"], d_o=c["d_o"],
+                                         dh_final=c["dh"], impl=impl)
+        assert all(g[n].dtype == dtype for n in ("dq", "dk", "dv")) and g["dh0"].dtype == torch.float32
+        check_backward(x, None, g)
+    g = dp.linear_attention_backward(c["q"], c["k"], c["v"], c["log_decay"], d_o=c["d_o"])
+    check_backward(x, None, g, use_h0=False, use_dh=False)
+    assert dp.linear_attention_backward(c["q"], c["k"], c["v"], c["log_decay"], d_o=c["d_o"],
+                                        want_dh0=False)["dh0"] is None
+
+
+PACKED = [([0, 1, 127, 128, 129, 0], 2, 64, 64), ([700, 3, 64, 0, 47], 3, 128, 128), ([1], 1, 32, 32),
+          ([0, 0], 2, 64, 32), ([256, 31, 513, 5], 2, 128, 64), ([33] * 20, 9, 32, 128), ([1700, 1], 1, 64, 128)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("lengths,H,Dk,Dv", PACKED, ids=str)
+def test_packed(dp, lengths, H, Dk, Dv, dtype):
+    """Every sequence on its own, empty ones among them; a bound on the
+    longest sequence that is larger than it changes nothing but rounding."""
+    T, N = sum(lengths), len(lengths)
+    x = draw((T, H), Dk, Dv, dtype, T + N, N, first=N)
+    c = {n: t.cuda() for n, t in x.items()}
+    for impl in impls(dp, dtype):
+        for bound in (None, T):
+            kw = dict(cu_seqlens=cu_of(lengths), max_seqlen=bound, impl=impl)
+            o, hf = dp.linear_attention_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["h0"], **kw)
+            check_forward(x, lengths, o, hf)
+            g = dp.linear_attention_backward_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["h0"], d_o=c["d_o"],
+                                                    dh_final=c["dh"], **kw)
+            check_backward(x, lengths, g)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_neighbours_do_not_leak(dp, dtype):
+    """NaN and infinity in one sequence of a packed batch, and in one head,
+    reach no other: the other outputs are bit for bit those of clean inputs."""
+    lengths, H = [130, 70, 300, 1, 0, 129], 3
+    T, N = sum(lengths), len(lengths)
+    x = draw((T, H), 64, 128, dtype, 5, N)
+    c = {n: t.cuda() for n, t in x.items()}
+    cu = cu_of(lengths)
+
+    def both():
+        o, hf = dp.linear_attention_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["h0"], cu_seqlens=cu,
+                                           max_seqlen=300)
+        g = dp.linear_attention_backward_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["h0"], d_o=c["d_o"],
+                                                dh_final=c["dh"], cu_seqlens=cu, max_seqlen=300)
+        return dict(o=o, hf=hf, **g)
+
+    clean = both()
+    for n in ("q", "k", "v", "d_o"):
+        c[n][200:500] = float("nan")          # the third sequence, every head
+        c[n][130:200, 1] = float("inf")       # the second one, one head
+    dirty = both()
+    for n in clean:
+        rows = clean[n].shape[0] == T
+        keep = [i for i in range(T) if i < 130 or i >= 500] if rows else [0, 3, 4, 5]
+        assert torch.equal(clean[n][keep], dirty[n][keep]), n
+        part = slice(130, 200) if rows else slice(1, 2)
+        assert torch.equal(clean[n][part][:, [0, 2]], dirty[n][part][:, [0, 2]]), n
+
+
+@pytest.mark.parametrize("cu", [[0, 40, 30, 100], [0, 40, 80, 101], [1, 40, 80, 100], [0, 90, 95, 100],
+                                [0, -5, 80, 100], [0, 40, 80, 99]], ids=str)
+def test_bad_offsets_are_reported(dp, cu):
+    """Offsets out of order, out of range, off the ends or longer than the
+    bound: the device reports it, sequences that break the rules keep their
+    outputs untouched, and the workspace is clean for the next call."""
+    H, N, T, bound = 2, 3, 100, 60
+    x = draw((T, H), 64, 64, torch.bfloat16, 9, N)
+    c = {n: t.cuda() for n, t in x.items()}
+    ws = torch.zeros(dp.linear_attention_workspace_size(N, T, H, 64, 64, max_seqlen=bound, backward=True),
+                     dtype=torch.uint8, device="cuda")
+    mark = 7.0
+    out = torch.full((T, H, 64), mark, dtype=torch.bfloat16, device="cuda")
+    hf = torch.full((N, H, 64, 64), mark, device="cuda")
+    bad = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    dp.linear_attention_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["h0"], cu_seqlens=bad, max_seqlen=bound,
+                               out=out, h_final=hf, workspace=ws)
+    with pytest.raises(dp.DPError) as e:
+        dp.check_status(ws)
+    assert e.value.code == 7
+    for s in range(N):
+        a, b = cu[s], cu[s + 1]
+        good = 0 <= a <= b <= T and b - a <= bound and (s > 0 or a == 0) and (s < N - 1 or b == T)
+        if not good:
+            assert (hf[s] == mark).all()
+    dp.linear_attention_backward_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["h0"], d_o=c["d_o"],
+                                        cu_seqlens=bad, max_seqlen=bound, workspace=ws)
+    with pytest.raises(dp.DPError):
+        dp.check_status(ws)
+    o, h = dp.linear_attention_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["h0"],
+                                      cu_seqlens=cu_of([40, 40, 20]), max_seqlen=bound, workspace=ws)
+    dp.check_status(ws)
+    check_forward(x, [40, 40, 20], o, h)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_empty_calls(dp, dtype):
+    """T = 0 hands the state through; no sequences or no heads is a no-op."""
+    for B, T, H in ((2, 0, 3), (0, 5, 2), (2, 5, 0)):
+        x = draw((B, T, H), 64, 32, dtype, 1, B)
+        c = {n: t.cuda() for n, t in x.items()}
+        o, hf = dp.linear_attention(c["q"], c["k"], c["v"], c["log_decay"], c["h0"])
+        assert o.shape == (B, T, H, 32)
+        g = dp.linear_attention_backward(c["q"], c["k"], c["v"], c["log_decay"], c["h0"], d_o=c["d_o"],
+                                         dh_final=c["dh"])
+        if T == 0:
+            assert torch.equal(hf, c["h0"]) and torch.equal(g["dh0"], c["dh"])
+            assert not dp.linear_attention(c["q"], c["k"], c["v"], c["log_decay"])[1].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,H,Dk,Dv", [(1, 1, 32, 32), (2, 6, 64, 128), (3, 16, 128, 128), (200, 3, 128, 32)], ids=str)
+def test_steps_follow_the_sequence(dp, B, H, Dk, Dv, dtype):
+    """Three steps on a carried state are a sequence of three tokens."""
+    x = draw((B, 3, H), Dk, Dv, dtype, 3, B)
+    c = {n: t.cuda() for n, t in x.items()}
+    state = c["h0"].clone()
+    o = torch.stack([dp.linear_attention_step(c["q"][:, t].contiguous(), c["k"][:, t].contiguous(),
+                                              c["v"][:, t].contiguous(), c["log_decay"], state)
+                     for t in range(3)], 1)
+    check_forward(x, None, o, state)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_calls_carry_on(dp, dtype):
+    """Two calls that hand the state on (h_final over h0, in place) give what
+    one call gives, and every call repeats itself bit for bit."""
+    B, T, H, D = 2, 700, 2, 64
+    x = draw((B, T, H), D, D, dtype, 11, B)
+    c = {n: t.cuda() for n, t in x.items()}
+    state, parts = c["h0"].clone(), []
+    for a, b in ((0, 333), (333, 700)):
+        cut = [c[n][:, a:b].contiguous() for n in ("q", "k", "v")]
+        parts.append(dp.linear_attention(*cut, c["log_decay"], state, h_final=state)[0])
+    check_forward(x, None, torch.cat(parts, 1), state)
+    first = dp.linear_attention(c["q"], c["k"], c["v"], c["log_decay"], c["h0"])
+    grads = dp.linear_attention_backward(c["q"], c["k"], c["v"], c["log_decay"], c["h0"], d_o=c["d_o"],
+                                         dh_final=c["dh"])
+    for _ in range(20):
+        again = dp.linear_attention(c["q"], c["k"], c["v"], c["log_decay"], c["h0"])
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+        more = dp.linear_attention_backward(c["q"], c["k"], c["v"], c["log_decay"], c["h0"], d_o=c["d_o"],
+                                            dh_final=c["dh"])
+        assert all(torch.equal(grads[n], more[n]) for n in grads)
+
+
+def test_long_memory_keeps_fp32_states(dp):
+    """A decay near 1 over many tokens: the state's error stays that of fp32
+    sums (4e-6 in RMS), the segments' states included."""
+    for impl in ("recurrent", "auto"):
+        x = draw((1, 6000, 2), 128, 128, torch.bfloat16, 13, 1)
+        x["log_decay"] = torch.tensor([-1 / 4096, -1 / 20000])
+        c = {n: t.cuda() for n, t in x.items()}
+        o, hf = dp.linear_attention(c["q"], c["k"], c["v"], c["log_decay"], c["h0"], impl=impl)
+        check_forward(x, None, o, hf)
+
+
+def test_other_stream(dp):
+    """Calls on a stream of their own order with that stream's work only."""
+    x = draw((2, 400, 2), 128, 128, torch.bfloat16, 17, 2)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        c = {n: t.cuda() for n, t in x.items()}
+        o, hf = dp.linear_attention(c["q"], c["k"], c["v"], c["log_decay"], c["h0"])
+    s.synchronize()
+    check_forward(x, None, o, hf)
+    o2, hf2 = dp.linear_attention(c["q"], c["k"], c["v"], c["log_decay"], c["h0"], stream=s)
+    s.synchronize()
+    assert torch.equal(o, o2) and torch.equal(hf, hf2)
+
+
+def test_gradients_match_differences(dp):
+    """<d_o, o> + <dh, h_final> is linear in each of q, k, v, h0: central
+    differences of the fp32 forward are exact up to its rounding, which for
+    the sum of B T H Dv products of size one is below 1e-4 of their root."""
+    B, T, H, Dk, Dv = 1, 150, 2, 64, 64
+    x = draw((B, T, H), Dk, Dv, torch.float32, 19, B)
+    c = {n: t.cuda() for n, t in x.items()}
+    g = dp.linear_attention_backward(c["q"], c["k"], c["v"], c["log_decay"], c["h0"], d_o=c["d_o"], dh_final=c["dh"])
+
+    def loss(y):
+        o, hf = dp.linear_attention(y["q"], y["k"], y["v"], y["log_decay"], y["h0"])
+        return float((o.double() * c["d_o"].double()).sum() + (hf.double() * c["dh"].double()).sum())
+
+    gen = torch.Generator().manual_seed(1)
+    for name, grad in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("h0", "dh0")):
+        step = torch.randn(x[name].shape, generator=gen).cuda()
+        up, dn = dict(c), dict(c)
+        up[name], dn[name] = c[name] + 0.5 * step, c[name] - 0.5 * step
+        want = loss(up) - loss(dn)
+        got = float((g[grad].double() * step.double()).sum())
+        assert abs(got - want) <= 1e-4 * np.sqrt(B * T * H * Dv) * max(1.0, abs(want) ** 0.5), (name, got, want)
+
+
+def test_refusals(dp):
+    q = torch.zeros(1, 4, 2, 64, device="cuda", dtype=torch.bfloat16)
+    ld = torch.zeros(2, device="cuda")
+    ok = dict(q=q, k=q, v=q, log_decay=ld)
+    for bad, err in ((dict(k=q[:, :3].contiguous()), ValueError), (dict(v=q.float()), TypeError),
+                     (dict(log_decay=ld.double()), TypeError), (dict(log_decay=ld[:1]), ValueError),
+                     (dict(h0=torch.zeros(1, 2, 64, 32, device="cuda")), ValueError),
+                     (dict(q=q.transpose(1, 2)), ValueError), (dict(out=q.float()), TypeError),
+                     (dict(h_final=torch.zeros(2, device="cuda")), ValueError),
+                     (dict(workspace=torch.zeros(8, device="cuda")), dp.DPError)):
+        with pytest.raises(err):
+            dp.linear_attention(**{**ok, **bad})
+    odd = torch.zeros(1, 4, 2, 48, device="cuda")
+    with pytest.raises(dp.DPError):
+        dp.linear_attention(odd, odd, odd, ld)
+    with pytest.raises(dp.DPError):   # fp32 has no tensor-core form
+        dp.linear_attention(q.float(), q.float(), q.float(), ld, impl="chunk_tc")
+    host = torch.zeros(1, 2, 64, 64)
+    with pytest.raises(ValueError):
+        dp.linear_attention(**ok, h0=host)

@@ -1,0 +1,124 @@
+"""Host-side refusals of the linear-attention and group-norm entry points (CPU
+only: none of these calls reaches a kernel) and their workspace queries."""
+import ctypes as C
+
+import pytest
+
+from deltaproduct_householder_product_gb300 import _lib
+
+OK, INVALID, UNSUPPORTED, ALIGNMENT, WORKSPACE = 0, 1, 2, 3, 4
+
+
+@pytest.fixture(scope="module")
+def L():
+    from deltaproduct_householder_product_gb300 import build
+    build.build()
+    return _lib.lib()
+
+
+def la(**kw):
+    d = dict(B=2, T=64, H=2, Dk=64, Dv=128, dtype=_lib.DP_BF16, impl=0, max_seqlen=0)
+    d.update(kw)
+    return _lib.LaDims(*[d[n] for n, _ in _lib.LaDims._fields_])
+
+
+def gn(**kw):
+    d = dict(N=4, S=3, C=64, G=4, dtype=_lib.DP_F32, act=1, eps=1e-5)
+    d.update(kw)
+    return _lib.GnDims(*[d[n] for n, _ in _lib.GnDims._fields_])
+
+
+def query(f, dims):
+    n = C.c_size_t(0)
+    return f(C.byref(dims) if dims is not None else None, C.byref(n)), n.value
+
+
+BAD_LA = [(dict(B=-1), INVALID), (dict(T=-1), INVALID), (dict(H=-1), INVALID), (dict(dtype=2), INVALID),
+          (dict(impl=3), INVALID), (dict(impl=-1), INVALID), (dict(max_seqlen=65), INVALID),
+          (dict(max_seqlen=-1), INVALID), (dict(Dk=48), UNSUPPORTED), (dict(Dv=256), UNSUPPORTED),
+          (dict(impl=2, dtype=_lib.DP_F32), UNSUPPORTED), (dict(B=1 << 20, H=1 << 12), UNSUPPORTED)]
+
+
+@pytest.mark.parametrize("bad,code", BAD_LA, ids=str)
+def test_linear_attention_dims(L, bad, code):
+    for f in (L.dp_linear_attention_workspace_size, L.dp_linear_attention_backward_workspace_size):
+        assert query(f, la(**bad))[0] == code
+    # the calls refuse the same dims, whatever the pointers
+    nulls = [None] * 8 + [C.c_size_t(0), None]
+    if "max_seqlen" not in bad:
+        assert L.dp_linear_attention(C.byref(la(**bad)), *nulls) == code
+    assert L.dp_linear_attention_varlen(C.byref(la(**{"max_seqlen": 64, **bad})), None, *nulls) == code
+
+
+def test_linear_attention_workspace(L):
+    for f in (L.dp_linear_attention_workspace_size, L.dp_linear_attention_backward_workspace_size):
+        rc, n = query(f, la())
+        assert rc == OK and n >= 256
+        assert query(f, None)[0] == INVALID
+        assert f(C.byref(la()), None) == INVALID
+        for empty in (dict(B=0), dict(T=0), dict(H=0)):
+            assert query(f, la(**empty))[0] == OK
+
+
+def test_linear_attention_pointers(L):
+    nulls = [None] * 8 + [C.c_size_t(0), None]
+    assert L.dp_linear_attention(C.byref(la()), *nulls) == INVALID
+    assert L.dp_linear_attention(None, *nulls) == INVALID
+    odd = [C.c_void_p(0x1001)] + [C.c_void_p(0x1000)] * 7
+    assert L.dp_linear_attention(C.byref(la()), *odd, 1 << 20, None) == ALIGNMENT
+    # a dense call takes no max_seqlen, a packed one needs offsets and a bound
+    assert L.dp_linear_attention(C.byref(la(max_seqlen=64)), *odd, 1 << 20, None) == INVALID
+    assert L.dp_linear_attention_varlen(C.byref(la(max_seqlen=64)), None, *odd, 1 << 20, None) == INVALID
+    assert L.dp_linear_attention_varlen(C.byref(la()), C.c_void_p(0x1000), *odd, 1 << 20, None) == INVALID
+    # nothing to do: no pointer is looked at
+    assert L.dp_linear_attention(C.byref(la(B=0)), *nulls) == OK
+    assert L.dp_linear_attention(C.byref(la(H=0)), *nulls) == OK
+    step = [None] * 6 + [None]
+    assert L.dp_linear_attention_step(C.byref(la()), *step) == INVALID
+    assert L.dp_linear_attention_step(C.byref(la(Dk=16)), *step) == UNSUPPORTED
+    assert L.dp_linear_attention_step(C.byref(la(B=0)), *step) == OK
+    back = [None] * 12 + [C.c_size_t(0), None]
+    assert L.dp_linear_attention_backward(C.byref(la()), *back) == INVALID
+    assert L.dp_linear_attention_backward(C.byref(la(B=0)), *back) == OK
+    assert L.dp_linear_attention_backward_varlen(C.byref(la(max_seqlen=64)), None, *back) == INVALID
+
+
+BAD_GN = [(dict(N=-1), INVALID), (dict(S=0), INVALID), (dict(C=0), INVALID), (dict(G=0), INVALID),
+          (dict(G=5), INVALID), (dict(dtype=2), INVALID), (dict(act=2), INVALID), (dict(eps=-1.0), INVALID),
+          (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID),
+          (dict(N=1 << 20, C=1 << 14, G=1 << 14), UNSUPPORTED), (dict(N=1 << 20, S=1 << 14), UNSUPPORTED)]
+
+
+@pytest.mark.parametrize("bad,code", BAD_GN, ids=str)
+def test_group_norm_dims(L, bad, code):
+    for f in (L.dp_group_norm_workspace_size, L.dp_group_norm_backward_workspace_size):
+        assert query(f, gn(**bad))[0] == code
+    assert L.dp_group_norm(C.byref(gn(**bad)), *([None] * 7), 0, None) == code
+    assert L.dp_group_norm_backward(C.byref(gn(**bad)), *([None] * 10), 0, None) == code
+
+
+def test_group_norm_pointers(L):
+    assert query(L.dp_group_norm_workspace_size, gn())[1] >= 256
+    assert query(L.dp_group_norm_workspace_size, None)[0] == INVALID
+    assert L.dp_group_norm(C.byref(gn()), *([None] * 7), 0, None) == INVALID
+    odd = [C.c_void_p(0x1004)] + [C.c_void_p(0x1000)] * 6
+    assert L.dp_group_norm(C.byref(gn()), *odd, 1 << 20, None) == ALIGNMENT
+    assert L.dp_group_norm(C.byref(gn(N=0)), *([None] * 7), 0, None) == OK
+    assert L.dp_group_norm_backward(C.byref(gn()), *([None] * 10), 0, None) == INVALID
+
+
+def test_python_refusals():
+    """Shapes, types and places are refused before the library is called."""
+    torch = pytest.importorskip("torch")
+    import deltaproduct_householder_product_gb300 as dp
+    q = torch.zeros(1, 4, 2, 32)
+    with pytest.raises(ValueError, match="CUDA"):
+        dp.linear_attention(q, q, q, torch.zeros(2))
+    with pytest.raises(ValueError, match=r"\[B,T,H,Dk\]"):
+        dp.linear_attention(q[0], q, q, torch.zeros(2))
+    with pytest.raises(ValueError, match=r"\[T,H,Dk\]"):
+        dp.linear_attention_varlen(q, q, q, torch.zeros(2), cu_seqlens=torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="act"):
+        dp.group_norm(q, groups=1, act="relu")
+    with pytest.raises(ValueError, match="CUDA"):
+        dp.group_norm(q, groups=1)
