@@ -496,17 +496,26 @@ dp_status check_la_dims(const dp_la_dims *d, bool step, bool varlen)
     if (!varlen && d->max_seqlen != 0) return DP_ERR_INVALID_ARG;
     if (varlen && (d->max_seqlen > d->T || (d->T > 0 && d->max_seqlen < 1))) return DP_ERR_INVALID_ARG;
     if (!supported_dim(d->Dk) || !supported_dim(d->Dv)) return DP_ERR_UNSUPPORTED;
+    // rows are counted in int, a segment's end past the last one included;
     // the grid is one CTA per sequence, head and segment
+    if (!step && d->T > (1 << 30)) return DP_ERR_UNSUPPORTED;
     if ((long long)d->B * d->H * dp::kLaMaxCluster > 0x7fffffffll) return DP_ERR_UNSUPPORTED;
-    if (d->impl == DP_IMPL_CHUNK_TC) return DP_ERR_UNSUPPORTED;
+    if (d->impl == DP_IMPL_CHUNK_TC && !dp::la_tc_supported(d->dtype)) return DP_ERR_UNSUPPORTED;
     return DP_OK;
 }
 
+bool la_tc(const dp_la_dims *d) { return d->impl != DP_IMPL_RECURRENT && dp::la_tc_supported(d->dtype); }
 bool la_varlen(const dp_la_dims *d) { return d && d->max_seqlen != 0; }
 
 int la_cluster(const dp_la_dims *d)
 {
-    return dp::la_simt_cluster(d->B, d->H, d->max_seqlen > 0 ? d->max_seqlen : d->T);
+    const int longest = d->max_seqlen > 0 ? d->max_seqlen : d->T;
+    return la_tc(d) ? dp::la_tc_cluster(d->B, d->H, longest) : dp::la_simt_cluster(d->B, d->H, longest);
+}
+
+cudaError_t la_launch(const dp_la_dims *d, const dp::LaPass &p)
+{
+    return la_tc(d) ? dp::launch_la_tc(p) : dp::launch_la_simt(p);
 }
 
 size_t la_workspace(const dp_la_dims *d)
@@ -553,7 +562,7 @@ dp_status la_forward(const dp_la_dims *dims, const int *cu, const void *q, const
     dp::LaPass p = la_pass(dims, cu, log_decay, workspace, stream);
     p.x = q; p.y = k; p.z = v; p.out = o;
     p.init = h0; p.fin = h_final;
-    return from_cuda(dp::launch_la_simt(p));
+    return from_cuda(la_launch(dims, p));
 }
 
 dp_status la_backward(const dp_la_dims *dims, const int *cu, const void *q, const void *k, const void *v,
@@ -575,15 +584,15 @@ dp_status la_backward(const dp_la_dims *dims, const int *cu, const void *q, cons
     p.Dx = dims->Dv; p.Dz = dims->Dk;
     p.x = d_o; p.y = v; p.z = k; p.out = dq;
     p.init = h0; p.state_t = true;
-    cudaError_t e = dp::launch_la_simt(p);
+    cudaError_t e = la_launch(dims, p);
     if (e != cudaSuccess) return from_cuda(e);
     p.x = v; p.y = d_o; p.z = q; p.out = dk;  // dk_t = G_t v_t
     p.init = dh_final; p.reverse = true;
-    if ((e = dp::launch_la_simt(p)) != cudaSuccess) return from_cuda(e);
+    if ((e = la_launch(dims, p)) != cudaSuccess) return from_cuda(e);
     p = base;                                 // dv_t = G_t^T k_t, and the only pass that writes dh0
     p.x = k; p.y = q; p.z = d_o; p.out = dv;
     p.init = dh_final; p.fin = dh0; p.reverse = true;
-    return from_cuda(dp::launch_la_simt(p));
+    return from_cuda(la_launch(dims, p));
 }
 
 }  // namespace

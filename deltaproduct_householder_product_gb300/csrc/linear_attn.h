@@ -47,6 +47,11 @@ constexpr int kLaMaxCluster = 8;
 int la_simt_cluster(int N, int H, int max_T);
 cudaError_t launch_la_simt(const LaPass &p);
 
+// Tensor-core kernel: bf16, any supported size.
+bool la_tc_supported(int dtype);
+int la_tc_cluster(int N, int H, int max_T);
+cudaError_t launch_la_tc(const LaPass &p);
+
 // One token: state <- gamma state + k v^T, o = state^T q.
 struct LaStep {
     int B, H, Dk, Dv, dtype;
