@@ -521,7 +521,7 @@ cudaError_t la_launch(const dp_la_dims *d, const dp::LaPass &p)
 size_t la_workspace(const dp_la_dims *d)
 {
     const int P = la_cluster(d);
-    return kStatusBlock + (P > 1 ? (size_t)d->B * d->H * P * d->Dk * d->Dv * sizeof(float) : 0);
+    return kStatusBlock + (P > 1 ? (size_t)d->B * d->H * P * dp::la_part_cells(d->Dk, d->Dv) * sizeof(float) : 0);
 }
 
 dp_status check_workspace(const void *workspace, size_t bytes, size_t need)

@@ -36,12 +36,20 @@ struct LaPass {
     const int *cu;             // packed sequences (NULL: dense)
     int max_T;                 // longest sequence
     int P;                     // CTAs (one cluster) per sequence and head
-    float *part;               // [N,H,P,Dx,Dz] states of the segments (P > 1)
+    float *part;               // states of the segments (P > 1): N H P la_part_cells(..) values
     uint32_t *status;
     cudaStream_t stream;
 };
 
 constexpr int kLaMaxCluster = 8;
+
+// fp32 values of one segment's state in the workspace (the tensor-core kernel
+// pads the state to 128 rows and at least 64 columns, in either orientation)
+inline size_t la_part_cells(int Dk, int Dv)
+{
+    const int d = Dk > Dv ? Dk : Dv;
+    return (size_t)128 * (d < 64 ? 64 : d);
+}
 
 // CUDA-core kernel: any supported size and type, fp32 arithmetic.
 int la_simt_cluster(int N, int H, int max_T);

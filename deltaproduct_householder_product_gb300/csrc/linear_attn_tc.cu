@@ -34,24 +34,27 @@ namespace {
 using namespace sm100;
 
 constexpr int kC = 128;
-constexpr int kThreads = 512;
-// warps 0-3 scores and output, 4-11 weighted keys and state, then one each:
-constexpr int kStateWarp = 4, kLoadWarp = 12, kOutMmaWarp = 13, kStateMmaWarp = 14, kStoreWarp = 15;
+constexpr int kThreads = 640;
+// warps 0-3 scores, 4-7 output, 8-15 weighted keys and state, then one each:
+constexpr int kOutWarp = 4, kStateWarp = 8, kLoadWarp = 16, kOutMmaWarp = 17, kStateMmaWarp = 18, kStoreWarp = 19;
 constexpr int kOutWarps = 4, kStateWarps = 8;
+// registers after the move: two warpgroups of 128 a thread, three of 72, out
+// of the 640 x 96 that the kernel is launched with
+constexpr int kMovedRegs = 2 * 128 * 128 + 3 * 128 * 72;
 constexpr uint32_t kTries = 1u << 22;
 constexpr uint32_t kSub = 16384;    // one [128 rows][64 columns] bf16 tile, 128-byte swizzle
 
 // TMEM columns (fp32 lanes = rows of the chunk, or of the state)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColA = 0;       // A, fp32; its bf16 form overwrites the first half
-constexpr uint32_t kColY = 128;     // w Y of 64 rows: three terms of 32 columns
+constexpr uint32_t kColY = 128;     // w Y of 32 rows, two buffers: three terms of 16 columns each
 constexpr uint32_t kColB = 224;
 constexpr uint32_t kColO = 352;
 
 enum {
     bFullX, bFullY = bFullX + 2, bFullZ = bFullY + 2, bEmptyX = bFullZ + 2, bEmptyY = bEmptyX + 2,
-    bEmptyZ = bEmptyY + 2, bAFull = bEmptyZ + 2, bAReady, bInterFull, bOutFull, bOutFree, bStaged, bStored,
-    bYReady, bYFree, bBFull, bStateReady, bZReady, bFinOut, bFinState, kBars
+    bEmptyZ = bEmptyY + 2, bAFull = bEmptyZ + 2, bAReady, bInterFull, bInterReady, bOutFull, bOutFree, bStaged, bStored,
+    bYReady, bYFree = bYReady + 2, bBFull = bYFree + 2, bBFree, bStateReady, bZReady, bFinOut, bFinState, kBars
 };
 
 template <int DXP, int DZP> struct Layout {
@@ -79,8 +82,9 @@ struct Params {
 struct Cta {
     uint8_t *base;
     uint64_t *bar;
-    float *pw;                    // gamma^0 .. gamma^128
-    float2 *pc;                   // gamma^128, gamma^(rows of the ragged chunk), as two fp32 each
+    uint32_t pw;                  // shared: gamma^0 .. gamma^128
+    uint32_t pr;                  // shared: gamma^31 .. gamma^0
+    uint32_t pc;                  // shared: gamma^128, gamma^(rows of the ragged chunk), as two fp32 each
     volatile uint32_t *abort;
     uint32_t *status;
     uint32_t tmem;
@@ -125,13 +129,30 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         : "memory");
 }
 
-// 16 lanes x 16 columns: register 2j holds lane t/4, column 4j + t%4,
+// 16 lanes x 8 columns: register 2j holds lane t/4, column 4j + t%4,
 // register 2j+1 the lane 8 above it
-__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t (&r)[8])
+__device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t (&r)[4])
 {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
                  : "memory");
+}
+
+__device__ __forceinline__ float lds(uint32_t a)
+{
+    float f;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(a));
+    return f;
+}
+__device__ __forceinline__ float4 lds4(uint32_t a)
+{
+    float4 f;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(a));
+    return f;
+}
+__device__ __forceinline__ void sts4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d)
@@ -203,22 +224,29 @@ __device__ void load_role(const Cta &c, const CUtensorMap *mx, const CUtensorMap
 }
 
 // ------------------------------------------------------------------ MMAs of scores and output
+// The issuing thread's own instructions are on the MMAs' path (an MMA takes
+// about 68 cycles): descriptors are built once and advanced by an addition
+// to their address field, and the loops over a whole chunk are unrolled.
 template <int DXP, int DZP, bool REV>
 __device__ void out_mma_role(const Cta &c)
 {
     using L = Layout<DXP, DZP>;
     const uint32_t base = smem_addr(c.base), dA = c.tmem + kColA, dO = c.tmem + kColO;
+    const uint64_t kmajor = sdesc_sw128(base, 0, 1024), zmajor = sdesc_sw128(base + L::off_z, kSub, 1024);
+    const uint64_t emajor = sdesc_sw128(base + L::off_e, L::e_sub, 1024);
     int inter = 0;
     for (int j = 0; j < c.chunks; ++j) {
         const int i = c.own_chunks + j, st = i & 1, live = c.live<REV>(j);
-        const uint32_t sx = base + st * L::stage, sy = sx + L::off_y, sz = sx + L::off_z;
+        const uint32_t stage = (uint32_t)st * (L::stage >> 4);
+        const uint64_t x = kmajor + stage, y = x + (L::off_y >> 4), z = zmajor + stage;
         if (!c.wait(bFullX + st, (j >> 1) & 1) || !c.wait(bFullY + st, (i >> 1) & 1)) break;
         // A's columns are free once the last chunk's A Z has completed
         if (j > 0 && !c.wait(bOutFull, (j - 1) & 1)) break;
         tc_fence_after();
+#pragma unroll
         for (int k = 0; k < DXP / 16; ++k)
-            mma_ss(dA, sdesc_sw128(sx + (k >> 2) * kSub + (k & 3) * 32, 0, 1024),
-                   sdesc_sw128(sy + (k >> 2) * kSub + (k & 3) * 32, 0, 1024), idesc_bf16(kC, kC, false, false), k > 0);
+            mma_ss(dA, x + ((k >> 2) * (kSub >> 4) + (k & 3) * 2), y + ((k >> 2) * (kSub >> 4) + (k & 3) * 2),
+                   idesc_bf16(kC, kC, false, false), k > 0);
         mma_commit(&c.bar[bAFull]);
         mma_commit(&c.bar[bEmptyY + st]);
         const bool state = c.has0 || j > 0;
@@ -226,19 +254,25 @@ __device__ void out_mma_role(const Cta &c)
         if (state) {
             if (!c.wait(bStateReady, inter & 1)) break;
             tc_fence_after();
+#pragma unroll
             for (int k = 0; k < DXP / 16; ++k)
-                mma_ss(dO, sdesc_sw128(sx + (k >> 2) * kSub + (k & 3) * 32, 0, 1024),
-                       sdesc_sw128(base + L::off_e + k * 2048, L::e_sub, 1024), idesc_bf16(kC, DZP, false, true), k > 0);
+                mma_ss(dO, x + ((k >> 2) * (kSub >> 4) + (k & 3) * 2), emajor + k * 128,
+                       idesc_bf16(kC, DZP, false, true), k > 0);
             mma_commit(&c.bar[bInterFull]);
-            ++inter;
         }
         if (!c.wait(bFullZ + st, (i >> 1) & 1)) break;
         if (c.packed && live < kC && !c.wait(bZReady, 0)) break;
+        if (state && !c.wait(bInterReady, inter++ & 1)) break;
         if (!c.wait(bAReady, j & 1)) break;
         tc_fence_after();
-        for (int k = 0; k < (live + 15) / 16; ++k)
-            mma_ts(dO, dA + k * 8, sdesc_sw128(sz + k * 2048, kSub, 1024), idesc_bf16(kC, DZP, false, true),
-                   state || k > 0);
+        if (live > kC - 16) {
+#pragma unroll
+            for (int k = 0; k < kC / 16; ++k)
+                mma_ts(dO, dA + k * 8, z + k * 128, idesc_bf16(kC, DZP, false, true), state || k > 0);
+        } else {
+            for (int k = 0; k < (live + 15) / 16; ++k)
+                mma_ts(dO, dA + k * 8, z + k * 128, idesc_bf16(kC, DZP, false, true), state || k > 0);
+        }
         mma_commit(&c.bar[bOutFull]);
         mma_commit(&c.bar[bEmptyZ + st]);
     }
@@ -248,27 +282,34 @@ __device__ void out_mma_role(const Cta &c)
 }
 
 // ------------------------------------------------------------------ MMAs of the state
+// B of a chunk in four quarters of 32 rows, which go through two TMEM buffers.
 template <int DXP, int DZP, bool REV>
 __device__ void state_mma_role(const Cta &c)
 {
     using L = Layout<DXP, DZP>;
-    const uint32_t base = smem_addr(c.base), dB = c.tmem + kColB, aY = c.tmem + kColY;
-    int half = 0;
+    const uint32_t dB = c.tmem + kColB, aY = c.tmem + kColY;
+    const uint64_t zmajor = sdesc_sw128(smem_addr(c.base) + L::off_z, kSub, 1024);
     for (int i = 0; i < c.own_chunks + c.updates; ++i) {
         const bool second = i >= c.own_chunks;
         const int st = i & 1, live = c.live<REV>(second ? i - c.own_chunks : i);
-        const uint32_t sz = base + st * L::stage + L::off_z;
+        const uint64_t z = zmajor + (uint32_t)st * (L::stage >> 4);
         if (!c.wait(bFullZ + st, (i >> 1) & 1)) break;
         bool ok = true;
-        for (int hh = 0; hh < 2; ++hh, ++half) {
-            if (!(ok = c.wait(bYReady, half & 1))) break;
+#pragma unroll
+        for (int qd = 0; qd < 4; ++qd) {
+            // buffer qd & 1 in its (2 i + qd / 2)-th use
+            if (!(ok = c.wait(bYReady + (qd & 1), (qd >> 1) & 1))) break;
+            if (qd == 0 && i > 0 && !(ok = c.wait(bBFree, (i - 1) & 1))) break;
             tc_fence_after();
-            const int rows = live - 64 * hh < 64 ? live - 64 * hh : 64;
+            const int rows = live - 32 * qd;
+#pragma unroll
             for (int term = 2; term >= 0; --term)
-                for (int k = 0; k < (rows + 15) / 16; ++k)
-                    mma_ts(dB, aY + term * 32 + k * 8, sdesc_sw128(sz + (4 * hh + k) * 2048, kSub, 1024),
-                           idesc_bf16(kC, DZP, false, true), hh > 0 || term < 2 || k > 0);
-            mma_commit(&c.bar[bYFree]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    if (rows > 16 * k)
+                        mma_ts(dB, aY + (qd & 1) * 48 + term * 16 + k * 8, z + (2 * qd + k) * 128,
+                               idesc_bf16(kC, DZP, false, true), qd > 0 || term < 2 || k > 0);
+            mma_commit(&c.bar[bYFree + (qd & 1)]);
         }
         if (!ok) break;
         mma_commit(&c.bar[bBFull]);
@@ -280,57 +321,82 @@ __device__ void state_mma_role(const Cta &c)
     mbar_wait(&c.bar[bFinState], 0, kTries, &none);
 }
 
-// ------------------------------------------------------------------ scores and output (lane = row of the chunk)
+// ------------------------------------------------------------------ scores (lane = row of the chunk)
 template <int DXP, int DZP, bool REV>
-__device__ void out_role(const Cta &c, __nv_bfloat16 *out, int H, int Dz)
+__device__ void score_role(const Cta &c)
 {
-    using L = Layout<DXP, DZP>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = 32 * warp + lane;
-    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-    const uint32_t tA = c.tmem + lanes + kColA, tO = c.tmem + lanes + kColO;
-    int inter = 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t tA = c.tmem + ((uint32_t)(32 * warp) << 16) + kColA;
     for (int j = 0; j < c.chunks; ++j) {
-        const int live = c.live<REV>(j), st = (c.own_chunks + j) & 1;
-        const bool state = c.has0 || j > 0;
+        const int live = c.live<REV>(j);
         if (!c.wait_warp(bAFull, j & 1)) return;
         tc_fence_after();
 #pragma unroll 1
         for (int b = 0; b < 4; ++b) {   // columns 32b .. 32b+31
-            uint32_t u[32], w[16];
+            uint32_t u[32];
             if (REV ? b < warp : b > warp) {
 #pragma unroll
-                for (int q = 0; q < 16; ++q) w[q] = 0;
+                for (int q = 0; q < 16; ++q) u[q] = 0;
             } else {
                 tmem_ld32(tA + 32 * b, u);
+                // |r - s| = [distance to the near edge of the column block] + [column within it]
+                float4 pq[2];
+                const float wr =
+                    b == warp ? 1.f : lds(c.pw + 4 * (REV ? 32 * (b - warp) - lane : 32 * (warp - b) + lane - 31));
                 tmem_wait_ld();
-                float f[32];
                 if (b == warp) {
 #pragma unroll
                     for (int q = 0; q < 32; ++q) {
                         const int far = REV ? q - lane : lane - q;
-                        f[q] = far >= 0 ? __uint_as_float(u[q]) * c.pw[far >= 0 ? far : 0] : 0.f;
+                        const float w = lds(c.pw + 4 * (far >= 0 ? far : 0));
+                        u[q] = far >= 0 ? __float_as_uint(__uint_as_float(u[q]) * w) : 0u;
                     }
                 } else {
-                    // |r - s| = [distance to the near edge of the column block] + [column within it]
-                    const float wr = c.pw[REV ? 32 * (b - warp) - lane : 32 * (warp - b) + lane - 31];
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) f[q] = __uint_as_float(u[q]) * (wr * c.pw[REV ? q : 31 - q]);
+                    for (int q = 0; q < 32; q += 8) {
+                        pq[0] = lds4((REV ? c.pw : c.pr) + 4 * q);
+                        pq[1] = lds4((REV ? c.pw : c.pr) + 4 * q + 16);
+                        const float w[8] = {pq[0].x, pq[0].y, pq[0].z, pq[0].w, pq[1].x, pq[1].y, pq[1].z, pq[1].w};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            u[q + e] = __float_as_uint(__uint_as_float(u[q + e]) * (wr * w[e]));
+                    }
                 }
                 if (REV && live < kC) {   // columns past the sequence are on the seen side here
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) f[q] = 32 * b + q < live ? f[q] : 0.f;
+                    for (int q = 0; q < 32; ++q) u[q] = 32 * b + q < live ? u[q] : 0u;
                 }
 #pragma unroll
-                for (int q = 0; q < 16; ++q) w[q] = pack_bf16x2(f[2 * q], f[2 * q + 1]);
+                for (int q = 0; q < 16; ++q)
+                    u[q] = pack_bf16x2(__uint_as_float(u[2 * q]), __uint_as_float(u[2 * q + 1]));
             }
+            uint32_t w[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) w[q] = u[q];
             // the fp32 columns that this overwrites (of blocks <= b) have been read
             tmem_st16(tA + 16 * b, w);
         }
-        if (state) {
+        tmem_wait_st();
+        tc_fence_before();
+        arrive_warp(&c.bar[bAReady]);
+    }
+}
+
+// ------------------------------------------------------------------ output (lane = row of the chunk)
+template <int DXP, int DZP, bool REV>
+__device__ void out_role(const Cta &c, __nv_bfloat16 *out, int H, int Dz)
+{
+    using L = Layout<DXP, DZP>;
+    const int warp = (threadIdx.x >> 5) - kOutWarp, lane = threadIdx.x & 31, r = 32 * warp + lane;
+    const uint32_t tO = c.tmem + ((uint32_t)(32 * warp) << 16) + kColO;
+    int inter = 0;
+    for (int j = 0; j < c.chunks; ++j) {
+        const int live = c.live<REV>(j), st = (c.own_chunks + j) & 1;
+        if (c.has0 || j > 0) {
             if (!c.wait_warp(bInterFull, inter++ & 1)) return;
             tc_fence_after();
             const int e = REV ? live - 1 - r : r + 1;
-            const float wr = e >= 0 ? c.pw[e] : 0.f;
+            const float wr = e >= 0 ? lds(c.pw + 4 * e) : 0.f;
 #pragma unroll 1
             for (int b = 0; b < DZP / 32; ++b) {
                 uint32_t u[32];
@@ -340,14 +406,14 @@ __device__ void out_role(const Cta &c, __nv_bfloat16 *out, int H, int Dz)
                 for (int q = 0; q < 32; ++q) u[q] = __float_as_uint(wr * __uint_as_float(u[q]));
                 tmem_st32(tO + 32 * b, u);
             }
+            tmem_wait_st();
+            tc_fence_before();
+            arrive_warp(&c.bar[bInterReady]);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        arrive_warp(&c.bar[bAReady]);
         if (!c.wait_warp(bOutFull, j & 1)) return;
         tc_fence_after();
         if (L::own_stage && j > 0 && !c.wait_warp(bStored, (j - 1) & 1)) return;
-        uint8_t *tile = c.base + (L::own_stage ? L::off_out : st * L::stage);
+        const uint32_t tile = smem_addr(c.base) + (L::own_stage ? L::off_out : st * L::stage);
 #pragma unroll 1
         for (int b = 0; b < DZP / 32; ++b) {
             uint32_t u[32];
@@ -355,12 +421,11 @@ __device__ void out_role(const Cta &c, __nv_bfloat16 *out, int H, int Dz)
             tmem_wait_ld();
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                uint4 v;
-                v.x = pack_bf16x2(__uint_as_float(u[8 * q]), __uint_as_float(u[8 * q + 1]));
-                v.y = pack_bf16x2(__uint_as_float(u[8 * q + 2]), __uint_as_float(u[8 * q + 3]));
-                v.z = pack_bf16x2(__uint_as_float(u[8 * q + 4]), __uint_as_float(u[8 * q + 5]));
-                v.w = pack_bf16x2(__uint_as_float(u[8 * q + 6]), __uint_as_float(u[8 * q + 7]));
-                *(uint4 *)(tile + (b >> 1) * kSub + sw128_offset(r, (b & 1) * 4 + q)) = v;
+                uint32_t v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = pack_bf16x2(__uint_as_float(u[8 * q + 2 * e]), __uint_as_float(u[8 * q + 2 * e + 1]));
+                sts4(tile + (b >> 1) * kSub + sw128_offset(r, (b & 1) * 4 + q), v[0], v[1], v[2], v[3]);
             }
         }
         tc_fence_before();
@@ -368,13 +433,13 @@ __device__ void out_role(const Cta &c, __nv_bfloat16 *out, int H, int Dz)
         if (c.packed && live < kC) {
             // the last rows of a packed sequence: no TMA store, which would
             // run on into the next sequence; each warp writes its own rows
-            __syncwarp();
+            const uint8_t *t = c.base + (L::own_stage ? L::off_out : st * L::stage);
             const int per = Dz / 8;
             for (int q = lane; q < 32 * per; q += 32) {
                 const int rr = 32 * warp + q / per, ch = q % per;
                 if (rr < live)
                     *(uint4 *)(out + ((c.g.row0 + c.row<REV>(j) + rr) * H + c.g.h) * Dz + ch * 8) =
-                        *(const uint4 *)(tile + (ch >> 3) * kSub + sw128_offset(rr, ch & 7));
+                        *(const uint4 *)(t + (ch >> 3) * kSub + sw128_offset(rr, ch & 7));
             }
         }
         fence_proxy_async_smem();
@@ -413,7 +478,6 @@ struct StateRole {
     bool live_rows;                          // this warp's rows are within DXP
     size_t head;
     float s[kN];
-    int half = 0;                            // halves of chunks sent so far
 
     __device__ __forceinline__ StateRole(const Cta &c_, const Params &p_) : c(c_), p(p_)
     {
@@ -468,35 +532,61 @@ struct StateRole {
         for (int q = 0; q < kN; ++q) s[q] = 0.f;
     }
 
-    // rows 64 hh + 32 side .. +31 of w Y, transposed into TMEM as three bf16 terms
-    __device__ __forceinline__ void send_keys(uint32_t sy, int hh, int live)
+    // the segment's own state, in an order of the threads' own
+    __device__ __forceinline__ void store_part(float *dst) const
     {
-        const int r0 = 64 * hh + 32 * side;
-        float w[8];
-        uint32_t keep[4];
+        float4 *d = (float4 *)dst + warp * 32 + lane;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            keep[q] = 0;
+        for (int q = 0; q < kN; q += 4)
+            d[(q / 4) * (kStateWarps * 32)] = make_float4(s[q], s[q + 1], s[q + 2], s[q + 3]);
+    }
+    __device__ __forceinline__ void add_part(const float *src, float w)
+    {
+        const float4 *d = (const float4 *)src + warp * 32 + lane;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = r0 + 8 * q + 2 * (lane & 3) + e, n = REV ? r + 1 : live - 1 - r;
-                const bool in = r < live;
-                w[2 * q + e] = in ? c.pw[n >= 0 ? n : 0] : 0.f;
-                keep[q] |= in ? 0xffffu << (16 * e) : 0u;   // rows past the sequence count as zeros
+        for (int b = 0; b < kN; b += 32) {
+            float4 v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = __ldcg(d + (b / 4 + q) * (kStateWarps * 32));
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                s[b + 4 * q] = fmaf(w, v[q].x, s[b + 4 * q]);
+                s[b + 4 * q + 1] = fmaf(w, v[q].y, s[b + 4 * q + 1]);
+                s[b + 4 * q + 2] = fmaf(w, v[q].z, s[b + 4 * q + 2]);
+                s[b + 4 * q + 3] = fmaf(w, v[q].w, s[b + 4 * q + 3]);
+            }
+        }
+    }
+
+    // quarter qd of w Y (rows 32 qd .. +31; this warp: 16 of them, 32 state
+    // rows), transposed into TMEM buffer qd & 1 as three bf16 terms
+    __device__ __forceinline__ void send_keys(uint32_t sy, int qd, int live)
+    {
+        const int r0 = 32 * qd + 16 * side;
+        float w[4];
+        uint32_t keep[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int r = r0 + 8 * q + 2 * (lane & 3);
+            if (r + 1 < live) {
+                w[2 * q] = lds(c.pw + 4 * (REV ? r + 1 : live - 1 - r));
+                w[2 * q + 1] = lds(c.pw + 4 * (REV ? r + 2 : live - 2 - r));
+                keep[q] = 0xffffffffu;
+            } else {   // rows past the sequence count as zeros
+                w[2 * q] = lds(c.pw + (REV && r < live ? 4 * (r + 1) : 0));
+                w[2 * q + 1] = 0.f;
+                keep[q] = r < live ? 0xffffu : 0u;
             }
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {    // 16 state rows each
             const int d = 32 * quarter + 16 * x;
-            const uint32_t sub = sy + (d >> 6) * kSub;
             const uint32_t chunk = ((d & 63) >> 3) + ((lane >> 3) & 1);
-            uint32_t hi[8], mid[8], lo[8];
+            uint32_t hi[4], mid[4], lo[4];
+            ldmatrix_x4_trans(sy + (d >> 6) * kSub + sw128_offset(r0 + 8 * (lane >> 4) + (lane & 7), chunk), hi[0],
+                              hi[1], hi[2], hi[3]);
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-                ldmatrix_x4_trans(sub + sw128_offset(r0 + 16 * q + 8 * (lane >> 4) + (lane & 7), chunk), hi[4 * q],
-                                  hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < 4; ++q) {
                 const uint32_t pair = hi[q] & keep[q >> 1];
                 const float a = __uint_as_float(pair << 16) * w[2 * (q >> 1)];
                 const float b = __uint_as_float(pair & 0xffff0000u) * w[2 * (q >> 1) + 1];
@@ -509,44 +599,61 @@ struct StateRole {
                 mid[q] = __byte_perm(__float_as_uint(a1), __float_as_uint(b1), 0x7632);
                 lo[q] = __byte_perm(__float_as_uint(a2), __float_as_uint(b2), 0x7632);
             }
-            const uint32_t t = c.tmem + ((uint32_t)d << 16) + kColY + 16 * side;
-            tmem_st_16x16(t, hi);
-            tmem_st_16x16(t + 32, mid);
-            tmem_st_16x16(t + 64, lo);
+            const uint32_t t = c.tmem + ((uint32_t)d << 16) + kColY + (qd & 1) * 48 + 8 * side;
+            tmem_st_16x8(t, hi);
+            tmem_st_16x8(t + 16, mid);
+            tmem_st_16x8(t + 32, lo);
         }
     }
 
-    // one chunk: w Y out, B in, E <- gamma^R E + B. Chunk i of all, j of its phase.
-    __device__ __forceinline__ bool chunk(int i, int j, bool first_phase)
+    // Quarter qd of chunk i (chunk j of its phase) into its buffer, once the
+    // MMAs of the buffer's last use have completed. The first quarter also
+    // waits for the chunk's rows.
+    __device__ __forceinline__ bool send(int i, int j, int qd)
     {
         const int st = i & 1, live = c.live<REV>(j);
-        if (!c.wait_warp(bFullY + st, (i >> 1) & 1)) return false;
-        if (c.packed && live < kC && !clear_tail(i, live)) return false;
-        for (int hh = 0; hh < 2; ++hh, ++half) {
-            if (half > 0 && !c.wait_warp(bYFree, (half - 1) & 1)) return false;
-            tc_fence_after();
-            if (live_rows) send_keys(smem_addr(c.base + st * L::stage + L::off_y), hh, live);
-            tmem_wait_st();
-            tc_fence_before();
-            arrive_warp(&c.bar[bYReady]);
+        if (qd == 0) {
+            if (!c.wait_warp(bFullY + st, (i >> 1) & 1)) return false;
+            if (c.packed && live < kC && !clear_tail(i, live)) return false;
         }
-        arrive_warp(&c.bar[bEmptyY + st]);
-        if (first_phase && warp == 0 && lane == 0) mbar_arrive(&c.bar[bEmptyY + st]);   // there is no X Y^T
+        // the buffer's use before this one: 2 i + qd / 2 - 1
+        if ((i > 0 || qd > 1) && !c.wait_warp(bYFree + (qd & 1), (qd >> 1) ^ 1)) return false;
+        tc_fence_after();
+        if (live_rows) send_keys(smem_addr(c.base + st * L::stage + L::off_y), qd, live);
+        tmem_wait_st();
+        tc_fence_before();
+        arrive_warp(&c.bar[bYReady + (qd & 1)]);
+        return true;
+    }
+
+    // Chunk i: its quarters, the next chunk's first quarter (next_j >= 0; it
+    // covers the wait for this one's MMAs), then E <- gamma^R E + B.
+    __device__ __forceinline__ bool chunk(int i, int j, bool first_phase, int next_j)
+    {
+        if (i == 0 && !send(i, j, 0)) return false;
+#pragma unroll 1
+        for (int qd = 1; qd < 4; ++qd)
+            if (!send(i, j, qd)) return false;
+        arrive_warp(&c.bar[bEmptyY + (i & 1)]);
+        if (first_phase && warp == 0 && lane == 0) mbar_arrive(&c.bar[bEmptyY + (i & 1)]);   // there is no X Y^T
+        if (next_j >= 0 && !send(i + 1, next_j, 0)) return false;
         if (!c.wait_warp(bBFull, i & 1)) return false;
         tc_fence_after();
         if (live_rows) {
-            const float2 w = live == kC ? c.pc[0] : c.pc[1];
+            const uint32_t pc = c.pc + (c.live<REV>(j) == kC ? 0 : 8);
+            const float wx = lds(pc), wy = lds(pc + 4);
 #pragma unroll
-            for (int b = 0; b < kN / 32; ++b) {
-                uint32_t u[32];
-                tmem_ld32(c.tmem + ((uint32_t)(32 * quarter) << 16) + kColB + dz0 + 32 * b, u);
+            for (int b = 0; b < kN / 16; ++b) {
+                uint32_t u[16];
+                tmem_ld16(c.tmem + ((uint32_t)(32 * quarter) << 16) + kColB + dz0 + 16 * b, u);
                 tmem_wait_ld();
 #pragma unroll
-                for (int q = 0; q < 32; ++q)
-                    s[32 * b + q] = fmaf(s[32 * b + q], w.x, fmaf(s[32 * b + q], w.y, __uint_as_float(u[q])));
+                for (int q = 0; q < 16; ++q)
+                    s[16 * b + q] = fmaf(s[16 * b + q], wx, fmaf(s[16 * b + q], wy, __uint_as_float(u[q])));
             }
         }
         tc_fence_before();
+        arrive_warp(&c.bar[bBFree]);
         return true;
     }
 
@@ -562,6 +669,7 @@ struct StateRole {
             *(uint4 *)(z + u * kSub + (live + (e >> 3)) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
+        if (i >= c.own_chunks) arrive_warp(&c.bar[bZReady]);   // for A Z; w Y's own signal follows
         return true;
     }
 
@@ -569,16 +677,12 @@ struct StateRole {
     __device__ __forceinline__ void publish()
     {
         if (live_rows) {
-            uint8_t *e = c.base + L::off_e + (DZP == 128 ? side * L::e_sub : 0);
+            const uint32_t e = smem_addr(c.base) + L::off_e + (DZP == 128 ? side * L::e_sub : 0);
 #pragma unroll
-            for (int q = 0; q < kN / 8; ++q) {
-                uint4 v;
-                v.x = pack_bf16x2(s[8 * q], s[8 * q + 1]);
-                v.y = pack_bf16x2(s[8 * q + 2], s[8 * q + 3]);
-                v.z = pack_bf16x2(s[8 * q + 4], s[8 * q + 5]);
-                v.w = pack_bf16x2(s[8 * q + 6], s[8 * q + 7]);
-                *(uint4 *)(e + sw128_offset(dx, (DZP == 128 ? 0 : 4 * side) + q)) = v;
-            }
+            for (int q = 0; q < kN / 8; ++q)
+                sts4(e + sw128_offset(dx, (DZP == 128 ? 0 : 4 * side) + q), pack_bf16x2(s[8 * q], s[8 * q + 1]),
+                     pack_bf16x2(s[8 * q + 2], s[8 * q + 3]), pack_bf16x2(s[8 * q + 4], s[8 * q + 5]),
+                     pack_bf16x2(s[8 * q + 6], s[8 * q + 7]));
         }
         fence_proxy_async_smem();
         arrive_warp(&c.bar[bStateReady]);
@@ -586,13 +690,14 @@ struct StateRole {
 
     __device__ __forceinline__ void run()
     {
-        const size_t cells = (size_t)p.Dx * p.Dz;
+        const size_t cells = (size_t)p.Dx * p.Dz, pad = (size_t)kN * kStateWarps * 32;
         const int last_rank = c.g.len > 0 ? (c.g.len - 1) / c.g.seg : 0;
         bool ok = true;
         clear();
-        for (int i = 0; i < c.own_chunks && ok; ++i) ok = chunk(i, i, true);
+        for (int i = 0; i < c.own_chunks && ok; ++i)
+            ok = chunk(i, i, true, i + 1 < c.own_chunks ? i + 1 : c.updates > 0 ? 0 : -1);
         if (p.P > 1) {
-            if (c.own_chunks > 0) store(p.part + (head * p.P + c.g.rank) * cells, false);
+            if (c.own_chunks > 0) store_part(p.part + (head * p.P + c.g.rank) * pad);
             __threadfence();
             cluster_arrive();
             cluster_wait();
@@ -605,8 +710,8 @@ struct StateRole {
         if (c.g.rank <= last_rank) {
             const int from = REV ? c.g.rank + 1 : 0, to = REV ? last_rank + 1 : c.g.rank;
             for (int q = from; q < to; ++q)
-                load_scaled(p.part + (head * p.P + q) * cells,
-                            la_power(ld, REV ? q * c.g.seg - c.g.end : c.g.begin - (q + 1) * c.g.seg), false);
+                add_part(p.part + (head * p.P + q) * pad,
+                         la_power(ld, REV ? q * c.g.seg - c.g.end : c.g.begin - (q + 1) * c.g.seg));
         }
         if (c.has0 && c.chunks > 0) publish();
         int inter = 0;
@@ -614,14 +719,10 @@ struct StateRole {
             const int i = c.own_chunks + j, live = c.live<REV>(j);
             if (j >= c.updates) {
                 // nothing reads the state after this chunk
-                if (c.packed && live < kC) {
-                    if (!clear_tail(i, live)) return;
-                    arrive_warp(&c.bar[bZReady]);
-                }
+                if (c.packed && live < kC && !clear_tail(i, live)) return;
                 break;
             }
-            if (!chunk(i, j, false)) return;
-            if (c.packed && live < kC) arrive_warp(&c.bar[bZReady]);
+            if (!chunk(i, j, false, j + 1 < c.updates ? j + 1 : -1)) return;
             if ((c.has0 || j > 0) && !c.wait_warp(bInterFull, inter++ & 1)) return;   // the last copy has been read
             if (j + 1 < c.chunks) publish();
         }
@@ -645,9 +746,12 @@ la_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
     }
     c.base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     c.bar = (uint64_t *)(c.base + L::off_aux);
-    c.pc = (float2 *)(c.bar + kBars);
-    c.pw = (float *)(c.pc + 2);
-    uint32_t *slot = (uint32_t *)(c.pw + kC + 1);
+    float *pw = (float *)(c.base + L::off_aux + 512), *pr = pw + 132;
+    float2 *pc = (float2 *)(pr + 32);
+    uint32_t *slot = (uint32_t *)(pc + 2);
+    c.pw = smem_addr(pw);
+    c.pr = smem_addr(pr);
+    c.pc = smem_addr(pc);
     c.abort = slot + 1;
     c.status = p.status;
     c.packed = p.cu != nullptr;
@@ -660,13 +764,15 @@ la_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float ld = p.log_decay[c.g.h];
-    if (threadIdx.x <= kC) c.pw[threadIdx.x] = la_power(ld, threadIdx.x);
-    if (threadIdx.x == 160) c.pc[0] = la_power2(ld, kC);
-    if (threadIdx.x == 192) c.pc[1] = la_power2(ld, c.g.len % kC);
+    if (threadIdx.x <= kC) pw[threadIdx.x] = la_power(ld, threadIdx.x);
+    else if (threadIdx.x >= 160 && threadIdx.x < 192) pr[threadIdx.x - 160] = la_power(ld, 191 - threadIdx.x);
+    else if (threadIdx.x == 192) pc[0] = la_power2(ld, kC);
+    else if (threadIdx.x == 224) pc[1] = la_power2(ld, c.g.len % kC);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBars; ++i) {
-            const int n = i == bAReady || i == bOutFree || i == bStaged ? kOutWarps
-                          : i == bYReady || i == bStateReady || i == bZReady ? kStateWarps
+            const int n = i == bAReady || i == bInterReady || i == bOutFree || i == bStaged ? kOutWarps
+                          : i == bYReady || i == bYReady + 1 || i == bBFree || i == bStateReady || i == bZReady
+                              ? kStateWarps
                           : i == bEmptyY || i == bEmptyY + 1 ? kStateWarps + 1
                           : i == bEmptyZ || i == bEmptyZ + 1 ? 2
                                                              : 1;
@@ -687,12 +793,17 @@ la_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
     tc_fence_after();
     c.tmem = *slot;
 
+    // registers move to the warps that hold the state (kMovedRegs)
+    if (warp >= kStateWarp && warp < kLoadWarp) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp >= kStateWarp && warp < kLoadWarp) {
         StateRole<DXP, DZP, REV> role(c, p);
         role.run();
     } else {
         if (p.P > 1) cluster_arrive();
-        if (warp < kStateWarp) {
+        if (warp < kOutWarp) {
+            score_role<DXP, DZP, REV>(c);
+        } else if (warp < kStateWarp) {
             out_role<DXP, DZP, REV>(c, out, p.H, p.Dz);
         } else if (lane == 0) {
             if (warp == kLoadWarp) load_role<DXP, DZP, REV>(c, &mx, &my, &mz);
@@ -722,6 +833,12 @@ cudaError_t launch_sized(const LaPass &p, const CUtensorMap (&m)[4])
 {
     auto kernel = la_tc_kernel<DXP, DZP, REV>;
     constexpr int smem = (int)Layout<DXP, DZP>::bytes;
+    // the register moves inside the kernel draw on what the launch allots
+    static const bool fits = [&] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, kernel) == cudaSuccess && a.numRegs * kThreads >= kMovedRegs;
+    }();
+    if (!fits) return cudaErrorLaunchOutOfResources;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const Params pr{p.N, p.T, p.H, p.Dx, p.Dz, p.max_T, p.P, p.log_decay, p.init, p.fin, p.part, p.cu, p.status,
