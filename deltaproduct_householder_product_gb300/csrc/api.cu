@@ -499,7 +499,7 @@ dp_status check_la_dims(const dp_la_dims *d, bool step, bool varlen)
     // rows are counted in int, a segment's end past the last one included;
     // the grid is one CTA per sequence, head and segment
     if (!step && d->T > (1 << 30)) return DP_ERR_UNSUPPORTED;
-    if ((long long)d->B * d->H * dp::kLaMaxCluster > 0x7fffffffll) return DP_ERR_UNSUPPORTED;
+    if ((long long)d->B * d->H * dp::kLaMaxSegments > 0x7fffffffll) return DP_ERR_UNSUPPORTED;
     if (d->impl == DP_IMPL_CHUNK_TC && !dp::la_tc_supported(d->dtype)) return DP_ERR_UNSUPPORTED;
     return DP_OK;
 }
@@ -507,10 +507,17 @@ dp_status check_la_dims(const dp_la_dims *d, bool step, bool varlen)
 bool la_tc(const dp_la_dims *d) { return d->impl != DP_IMPL_RECURRENT && dp::la_tc_supported(d->dtype); }
 bool la_varlen(const dp_la_dims *d) { return d && d->max_seqlen != 0; }
 
-int la_cluster(const dp_la_dims *d)
+int la_segments(const dp_la_dims *d)
 {
     const int longest = d->max_seqlen > 0 ? d->max_seqlen : d->T;
-    return la_tc(d) ? dp::la_tc_cluster(d->B, d->H, longest) : dp::la_simt_cluster(d->B, d->H, longest);
+    if (!la_tc(d)) return dp::la_simt_cluster(d->B, d->H, longest);
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 1;   // no device: one segment, which every device can run
+    }
+    return dp::la_tc_segments(d->B, d->H, d->T, longest, d->max_seqlen > 0, sms);
 }
 
 cudaError_t la_launch(const dp_la_dims *d, const dp::LaPass &p)
@@ -520,7 +527,7 @@ cudaError_t la_launch(const dp_la_dims *d, const dp::LaPass &p)
 
 size_t la_workspace(const dp_la_dims *d)
 {
-    const int P = la_cluster(d);
+    const int P = la_segments(d);
     return kStatusBlock + (P > 1 ? (size_t)d->B * d->H * P * dp::la_part_cells(d->Dk, d->Dv) * sizeof(float) : 0);
 }
 
@@ -540,7 +547,7 @@ dp::LaPass la_pass(const dp_la_dims *d, const int *cu, const float *log_decay, v
     p.log_decay = log_decay;
     p.cu = cu;
     p.max_T = d->max_seqlen > 0 ? d->max_seqlen : d->T;
-    p.P = la_cluster(d);
+    p.P = la_segments(d);
     p.status = (uint32_t *)workspace;
     p.part = (float *)((char *)workspace + kStatusBlock);
     p.stream = (cudaStream_t)stream;

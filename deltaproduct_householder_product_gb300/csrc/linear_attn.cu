@@ -171,6 +171,9 @@ la_simt_kernel(LaPass p)
         }
     }
 
+    // the final state may go where the initial one was: not before every
+    // segment has read that
+    if (p.P > 1) cluster_arrive();
     for (int i = 0; i < chunks; ++i) {
         const int c = rev ? chunks - 1 - i : i, row = g.begin + c * kC;
         const int live = g.end - row < kC ? g.end - row : kC;
@@ -256,6 +259,7 @@ la_simt_kernel(LaPass p)
         update(live);
         __syncthreads();
     }
+    if (p.P > 1) cluster_wait();
     if (p.fin && g.rank == (rev ? 0 : last_rank))
 #pragma unroll
         for (int a = 0; a < L::NX; ++a)

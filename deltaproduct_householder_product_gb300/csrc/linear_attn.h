@@ -35,13 +35,13 @@ struct LaPass {
     bool reverse;
     const int *cu;             // packed sequences (NULL: dense)
     int max_T;                 // longest sequence
-    int P;                     // CTAs (one cluster) per sequence and head
+    int P;                     // segments of a sequence, one CTA each
     float *part;               // states of the segments (P > 1): N H P la_part_cells(..) values
     uint32_t *status;
     cudaStream_t stream;
 };
 
-constexpr int kLaMaxCluster = 8;
+constexpr int kLaMaxCluster = 8, kLaMaxSegments = 32;
 
 // fp32 values of one segment's state in the workspace (the tensor-core kernel
 // pads the state to 128 rows and at least 64 columns, in either orientation)
@@ -51,13 +51,14 @@ inline size_t la_part_cells(int Dk, int Dv)
     return (size_t)128 * (d < 64 ? 64 : d);
 }
 
-// CUDA-core kernel: any supported size and type, fp32 arithmetic.
+// CUDA-core kernel: any supported size and type, fp32 arithmetic; a sequence's
+// segments are one cluster.
 int la_simt_cluster(int N, int H, int max_T);
 cudaError_t launch_la_simt(const LaPass &p);
 
 // Tensor-core kernel: bf16, any supported size.
 bool la_tc_supported(int dtype);
-int la_tc_cluster(int N, int H, int max_T);
+int la_tc_segments(int N, int H, int T, int max_T, bool packed, int sms);
 cudaError_t launch_la_tc(const LaPass &p);
 
 // One token: state <- gamma state + k v^T, o = state^T q.
@@ -71,7 +72,7 @@ struct LaStep {
 };
 cudaError_t launch_la_step(const LaStep &p);
 
-// ---- the part of a sequence that one CTA of a cluster runs: rows
+// ---- the part of a sequence that one CTA runs: rows
 // [begin, end) of the sequence, in segments of whole chunks
 struct LaSegment {
     int n, h;            // sequence, head

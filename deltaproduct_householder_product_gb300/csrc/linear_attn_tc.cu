@@ -20,13 +20,16 @@
 // is the sum of three MMAs, the small terms first. The MMAs only add within
 // a chunk; the sum over chunks is an fp32 multiply-add in registers.
 //
-// One CTA runs one segment of one (sequence, head). With P > 1 a cluster of P
-// CTAs holds the segments of one sequence: each first runs B and E alone over
-// its rows, the segments' states go through global memory, and each CTA then
-// starts from the decayed sum of those before it.
+// Where sequences and heads are too few for the SMs, each sequence is cut into
+// P segments: la_state_kernel runs B and E alone over the segments that others
+// follow, la_tc_kernel then starts every segment from the decayed sum of the
+// states before it (two launches; rows that stay in L2 are read from there
+// the second time).
 #include "linear_attn.h"
 #include "sm100.cuh"
 #include "tensor_map.h"
+
+#include <math.h>
 
 namespace dp {
 namespace {
@@ -34,41 +37,9 @@ namespace {
 using namespace sm100;
 
 constexpr int kC = 128;
-constexpr int kThreads = 640;
-// warps 0-3 scores, 4-7 output, 8-15 weighted keys and state, then one each:
-constexpr int kOutWarp = 4, kStateWarp = 8, kLoadWarp = 16, kOutMmaWarp = 17, kStateMmaWarp = 18, kStoreWarp = 19;
-constexpr int kOutWarps = 4, kStateWarps = 8;
-// registers after the move: two warpgroups of 128 a thread, three of 72, out
-// of the 640 x 96 that the kernel is launched with
-constexpr int kMovedRegs = 2 * 128 * 128 + 3 * 128 * 72;
 constexpr uint32_t kTries = 1u << 22;
 constexpr uint32_t kSub = 16384;    // one [128 rows][64 columns] bf16 tile, 128-byte swizzle
-
-// TMEM columns (fp32 lanes = rows of the chunk, or of the state)
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColA = 0;       // A, fp32; its bf16 form overwrites the first half
-constexpr uint32_t kColY = 128;     // w Y of 32 rows, two buffers: three terms of 16 columns each
-constexpr uint32_t kColB = 224;
-constexpr uint32_t kColO = 352;
-
-enum {
-    bFullX, bFullY = bFullX + 2, bFullZ = bFullY + 2, bEmptyX = bFullZ + 2, bEmptyY = bEmptyX + 2,
-    bEmptyZ = bEmptyY + 2, bAFull = bEmptyZ + 2, bAReady, bInterFull, bInterReady, bOutFull, bOutFree, bStaged, bStored,
-    bYReady, bYFree = bYReady + 2, bBFull = bYFree + 2, bBFree, bStateReady, bZReady, bFinOut, bFinState, kBars
-};
-
-template <int DXP, int DZP> struct Layout {
-    static constexpr int nx = DXP / 64, nz = DZP / 64;
-    static constexpr bool own_stage = DZP > DXP;           // else the output tile goes over X's
-    static constexpr uint32_t stage = (2 * nx + nz) * kSub;
-    static constexpr uint32_t off_y = nx * kSub, off_z = 2 * nx * kSub;
-    static constexpr uint32_t off_e = 2 * stage;           // bf16 state [DXP][DZP]
-    static constexpr uint32_t e_sub = DXP * 128;
-    static constexpr uint32_t off_out = off_e + nz * e_sub;
-    static constexpr uint32_t off_aux = off_out + (own_stage ? nz * kSub : 0);
-    static constexpr uint32_t aux = 2048;
-    static constexpr uint32_t bytes = off_aux + aux + 1024;
-};
+constexpr int kStateWarps = 16;     // four warpgroups: a quarter of a chunk's keys, of the state's columns each
 
 struct Params {
     int N, T, H, Dx, Dz, max_T, P;
@@ -79,21 +50,22 @@ struct Params {
     int state_t;
 };
 
+// What both kernels' roles share: one segment of one (sequence, head).
 struct Cta {
     uint8_t *base;
     uint64_t *bar;
     uint32_t pw;                  // shared: gamma^0 .. gamma^128
-    uint32_t pr;                  // shared: gamma^31 .. gamma^0
+    uint32_t pr;                  // shared: gamma^15 .. gamma^0
     uint32_t pc;                  // shared: gamma^128, gamma^(rows of the ragged chunk), as two fp32 each
     volatile uint32_t *abort;
     uint32_t *status;
     uint32_t tmem;
     LaSegment g;
+    int last_rank;                // the segment that holds the sequence's last row
     int chunks;                   // of this segment
-    int own_chunks;               // chunks of the first phase (the segment's own state), 0 or `chunks`
+    int updates;                  // of them, those whose rows go into the state
     bool has0;                    // a state enters the segment
     bool packed;
-    int updates;                  // chunks of the second phase that update the state
 
     __device__ __forceinline__ bool wait(int b, uint32_t parity) const
     {
@@ -107,7 +79,7 @@ struct Cta {
     {
         return __all_sync(0xffffffffu, wait(b, parity));
     }
-    // chunk i of a phase in processing order: its first row, live rows
+    // chunk i in processing order: its first row, live rows
     template <bool REV> __device__ __forceinline__ int row(int i) const
     {
         return g.begin + (REV ? chunks - 1 - i : i) * kC;
@@ -117,42 +89,87 @@ struct Cta {
         const int n = g.end - row<REV>(i);
         return n < kC ? n : kC;
     }
+    // the chunk that holds the last rows of a packed sequence: its tile runs
+    // on into the next sequence
+    __device__ __forceinline__ bool tail(int rows) const { return packed && rows < kC; }
 };
 
-// D[tmem] (+)= A[tmem, bf16 pairs] * B[smem desc]; issued by one thread
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+constexpr uint32_t kAuxBytes = 2048, kAuxTables = 512;   // barriers, then the decay tables
+
+// Tables, barriers' shared memory and the segment; called by every thread
+// before the first barrier. Returns the TMEM address slot.
+__device__ __forceinline__ uint32_t *setup(Cta &c, const Params &p, uint32_t off_aux)
+{
+    c.bar = (uint64_t *)(c.base + off_aux);
+    float *pw = (float *)(c.base + off_aux + kAuxTables), *pr = pw + 132;
+    float2 *pc = (float2 *)(pr + 16);
+    uint32_t *slot = (uint32_t *)(pc + 2);
+    c.pw = smem_addr(pw);
+    c.pr = smem_addr(pr);
+    c.pc = smem_addr(pc);
+    c.abort = slot + 1;
+    c.status = p.status;
+    c.packed = p.cu != nullptr;
+    c.chunks = (c.g.end - c.g.begin + kC - 1) / kC;
+    c.last_rank = c.g.len > 0 ? (c.g.len - 1) / c.g.seg : 0;
+    const float ld = p.log_decay[c.g.h];
+    if (threadIdx.x <= kC) pw[threadIdx.x] = la_power(ld, threadIdx.x);
+    else if (threadIdx.x >= 160 && threadIdx.x < 176) pr[threadIdx.x - 160] = la_power(ld, 175 - threadIdx.x);
+    else if (threadIdx.x == 192) pc[0] = la_power2(ld, kC);
+    else if (threadIdx.x == 224) pc[1] = la_power2(ld, c.g.len % kC);
+    if (threadIdx.x == 0) *c.abort = 0;
+    return slot;
+}
+
+// ------------------------------------------------------------------ instructions
+// The MMA roles run as whole warps and elect the issuing thread inside the
+// instruction's own block, and everything that steers them is broadcast from
+// lane 0 first: so the compiler knows the control flow and the descriptors to
+// be the same in all lanes and keeps the latter in the uniform registers that
+// the instruction takes.
+__device__ __forceinline__ int uni(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ uint64_t uni(uint64_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// D[tmem] (+)= A[smem desc] * B[smem desc]
+__device__ __forceinline__ void warp_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// D[tmem] (+)= A[tmem, bf16 pairs] * B[smem desc]
+__device__ __forceinline__ void warp_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-
-// 16 lanes x 8 columns: register 2j holds lane t/4, column 4j + t%4,
-// register 2j+1 the lane 8 above it
-__device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t (&r)[4])
+__device__ __forceinline__ void warp_commit(uint64_t *bar)
 {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3])
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
+        : "memory");
+}
+
+// 16 lanes x 16 columns: register 2j holds lane t/4, column 4j + t%4,
+// register 2j+1 the lane 8 above it
+__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
-
-__device__ __forceinline__ float lds(uint32_t a)
+// 32 lanes x 8 columns
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 {
-    float f;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(a));
-    return f;
-}
-__device__ __forceinline__ float4 lds4(uint32_t a)
-{
-    float4 f;
-    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(a));
-    return f;
-}
-__device__ __forceinline__ void sts4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
-{
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d)
@@ -161,6 +178,25 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t &a, ui
                  : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
                  : "r"(addr)
                  : "memory");
+}
+
+// Reads of the decay tables, which do not change after the kernel's first
+// barrier: not volatile, so that they are issued together ahead of their uses.
+__device__ __forceinline__ float lds(uint32_t a)
+{
+    float f;
+    asm("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(a));
+    return f;
+}
+__device__ __forceinline__ float4 lds4(uint32_t a)
+{
+    float4 f;
+    asm("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(a));
+    return f;
+}
+__device__ __forceinline__ void sts4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void *src, int c0, int c1, int c2, int c3)
@@ -177,106 +213,445 @@ __device__ __forceinline__ void arrive_warp(uint64_t *bar)
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// ------------------------------------------------------------------ loads
+// ------------------------------------------------------------------ the state's warps
+// Sixteen warps: lane = row of the state (32 rows for each quarter of a
+// warpgroup), warpgroup = a quarter of its columns, and a quarter (32 rows) of
+// a chunk's keys. The roles' loops are kept small on purpose: several roles
+// share an SM's instruction caches, and code unrolled over a chunk spent more
+// time fetching instructions than executing them.
 template <int DXP, int DZP, bool REV>
-__device__ void load_role(const Cta &c, const CUtensorMap *mx, const CUtensorMap *my, const CUtensorMap *mz)
+struct State {
+    static constexpr int kN = DZP / 4;       // state columns of a thread
+    const Cta &c;
+    const Params &p;
+    int warp, lane, quarter, group, dx, dz0;
+    bool live_rows;                          // this warp's state rows are within DXP
+    size_t head;
+    float s[kN];
+
+    // `first`: the kernel's first state warp
+    __device__ __forceinline__ State(const Cta &c_, const Params &p_, int first) : c(c_), p(p_)
+    {
+        warp = (threadIdx.x >> 5) - first;
+        lane = threadIdx.x & 31;
+        quarter = warp & 3;
+        group = warp >> 2;
+        dx = 32 * quarter + lane;
+        dz0 = group * kN;
+        live_rows = 32 * quarter < DXP;
+        head = (size_t)c.g.n * p.H + c.g.h;
+    }
+
+    // the caller's states, [N,H,Dx,Dz] or transposed: once per segment
+    __device__ __forceinline__ void load(const float *src, float w)
+    {
+        src += head * p.Dx * p.Dz;
+        const int step = p.state_t ? p.Dx : 1;
+        src += p.state_t ? (size_t)dz0 * p.Dx + dx : (size_t)dx * p.Dz + dz0;
+#pragma unroll
+        for (int q = 0; q < kN; ++q) s[q] = dx < p.Dx && dz0 + q < p.Dz ? w * __ldcg(src + (size_t)q * step) : 0.f;
+    }
+    __device__ __forceinline__ void store(float *dst) const
+    {
+        dst += head * p.Dx * p.Dz;
+        const int step = p.state_t ? p.Dx : 1;
+        dst += p.state_t ? (size_t)dz0 * p.Dx + dx : (size_t)dx * p.Dz + dz0;
+#pragma unroll
+        for (int q = 0; q < kN; ++q)
+            if (dx < p.Dx && dz0 + q < p.Dz) dst[(size_t)q * step] = s[q];
+    }
+    // a segment's state in the workspace, in an order of the threads' own
+    __device__ __forceinline__ float4 *part(int slot) const
+    {
+        return (float4 *)(p.part + (head * p.P + slot) * (kN * kStateWarps * 32)) + warp * 32 + lane;
+    }
+    __device__ __forceinline__ void store_part(int slot) const
+    {
+        float4 *d = part(slot);
+#pragma unroll
+        for (int q = 0; q < kN; q += 4)
+            d[(q / 4) * (kStateWarps * 32)] = make_float4(s[q], s[q + 1], s[q + 2], s[q + 3]);
+    }
+    __device__ __forceinline__ void add_part(int slot, float w)
+    {
+        const float4 *d = part(slot);
+        float4 v[kN / 4];
+#pragma unroll
+        for (int q = 0; q < kN / 4; ++q) v[q] = __ldcg(d + q * (kStateWarps * 32));
+#pragma unroll
+        for (int q = 0; q < kN / 4; ++q) {
+            s[4 * q] = fmaf(w, v[q].x, s[4 * q]);
+            s[4 * q + 1] = fmaf(w, v[q].y, s[4 * q + 1]);
+            s[4 * q + 2] = fmaf(w, v[q].z, s[4 * q + 2]);
+            s[4 * q + 3] = fmaf(w, v[q].w, s[4 * q + 3]);
+        }
+    }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int q = 0; q < kN; ++q) s[q] = 0.f;
+    }
+
+    // Quarter `group` of w Y (32 rows by this warp's 32 state rows) from the
+    // tile at sy, transposed into the TMEM columns at `col` as three bf16
+    // terms of 16 columns each.
+    __device__ __forceinline__ void send_keys(uint32_t sy, uint32_t col, int live) const
+    {
+        const int first = 32 * group + 2 * (lane & 3);
+        float w[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int r = first + 8 * (q >> 1) + (q & 1);
+            w[q] = lds(c.pw + 4 * (REV ? r + 1 : r < live ? live - 1 - r : 0));
+        }
+        // 8 x 8 blocks: two along the rows by two along the state rows
+        const uint32_t row = sy + (quarter >> 1) * kSub + (32 * group + 8 * (lane >> 4) + (lane & 7)) * 128;
+        const uint32_t piece = (uint32_t)((quarter & 1) * 4 + ((lane >> 3) & 1)), flip = lane & 7;
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {    // 16 state rows each
+            uint32_t hi[8], mid[8], lo[8];
+            ldmatrix_x4_trans(row + (((piece + 2 * x) ^ flip) << 4), hi[0], hi[1], hi[2], hi[3]);
+            ldmatrix_x4_trans(row + 2048 + (((piece + 2 * x) ^ flip) << 4), hi[4], hi[5], hi[6], hi[7]);
+            if (live < kC) {   // rows past the sequence count as zeros
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int r = first + 8 * (q >> 1);
+                    hi[q] &= (r < live ? 0xffffu : 0u) | (r + 1 < live ? 0xffff0000u : 0u);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const float a = __uint_as_float(hi[q] << 16) * w[2 * (q >> 1)];
+                const float b = __uint_as_float(hi[q] & 0xffff0000u) * w[2 * (q >> 1) + 1];
+                // the top 8 bits of what is left, three times: 24 in all
+                const float a1 = a - __uint_as_float(__float_as_uint(a) & 0xffff0000u);
+                const float b1 = b - __uint_as_float(__float_as_uint(b) & 0xffff0000u);
+                const float a2 = a1 - __uint_as_float(__float_as_uint(a1) & 0xffff0000u);
+                const float b2 = b1 - __uint_as_float(__float_as_uint(b1) & 0xffff0000u);
+                hi[q] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+                mid[q] = __byte_perm(__float_as_uint(a1), __float_as_uint(b1), 0x7632);
+                lo[q] = __byte_perm(__float_as_uint(a2), __float_as_uint(b2), 0x7632);
+            }
+            const uint32_t t = col + ((uint32_t)(32 * quarter + 16 * x) << 16);
+            tmem_st_16x16(t, hi);
+            tmem_st_16x16(t + 16, mid);
+            tmem_st_16x16(t + 32, lo);
+        }
+    }
+
+    // E <- gamma^R E + B, B in the TMEM columns at `col`
+    __device__ __forceinline__ void update(uint32_t col, int live)
+    {
+        const uint32_t pc = c.pc + (live == kC ? 0 : 8);
+        const float wx = lds(pc), wy = lds(pc + 4);
+#pragma unroll
+        for (int b = 0; b < kN / 16; ++b) {
+            uint32_t u[16];
+            tmem_ld16(col + ((uint32_t)(32 * quarter) << 16) + dz0 + 16 * b, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                s[16 * b + q] = fmaf(s[16 * b + q], wx, fmaf(s[16 * b + q], wy, __uint_as_float(u[q])));
+        }
+    }
+
+    // The rows of Z past the end of a packed sequence belong to the next one:
+    // they count as zeros (A and w Y are zero there, but zero times NaN is not).
+    __device__ __forceinline__ void clear_tail(uint8_t *z, int live) const
+    {
+        for (int q = warp * 32 + lane; q < (kC - live) * 8 * (DZP / 64); q += kStateWarps * 32) {
+            const int u = q / ((kC - live) * 8), e = q - u * (kC - live) * 8;
+            *(uint4 *)(z + u * kSub + (live + (e >> 3)) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+    }
+};
+
+// The MMAs of a quarter of B: three terms of 16 columns at aY against the 32
+// rows of Z at `z`; `rows` live ones.
+template <int DZP>
+__device__ __forceinline__ void state_mmas(uint32_t dB, uint32_t aY, uint64_t z, int rows, bool first)
+{
+#pragma unroll
+    for (int term = 2; term >= 0; --term)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (rows > 16 * k)
+                warp_mma_ts(dB, aY + term * 16 + k * 8, z + k * 128, idesc_bf16(kC, DZP, false, true),
+                            !first || term < 2 || k > 0);
+}
+
+// ================================================================== the segments' states
+namespace seg {
+
+constexpr int kThreads = 576;            // 16 state warps, loads, MMAs
+constexpr int kLoadWarp = 16, kMmaWarp = 17, kStages = 3;
+constexpr uint32_t kColB = 0, kColY = 256, kTmemCols = 512;   // two sums; w Y of each quarter
+enum {
+    bFullY, bFullZ = bFullY + kStages, bEmptyY = bFullZ + kStages, bEmptyZ = bEmptyY + kStages,
+    bYReady = bEmptyZ + kStages, bYFree = bYReady + 4, bBFull = bYFree + 4, bBFree = bBFull + 2, bZReady = bBFree + 2,
+    bFin, kBars
+};
+static_assert(kBars * 8 <= kAuxTables, "");
+
+template <int DXP, int DZP> struct Layout {
+    static constexpr int nx = DXP / 64, nz = DZP / 64;
+    static constexpr uint32_t stage = (nx + nz) * kSub, off_z = nx * kSub;
+    static constexpr uint32_t off_aux = kStages * stage, bytes = off_aux + kAuxBytes + 1024;
+};
+
+template <int DXP, int DZP, bool REV>
+__device__ void load_role(const Cta &c, const CUtensorMap *my, const CUtensorMap *mz)
 {
     using L = Layout<DXP, DZP>;
-    const int b = c.packed ? 0 : c.g.n;
-    const int t0 = c.packed ? (int)c.g.row0 : 0;
-    const int total = c.own_chunks + c.chunks;
-    bool ok = true;
+    const int b = c.packed ? 0 : c.g.n, t0 = c.packed ? (int)c.g.row0 : 0;
     int i = 0;
-    for (; i < total && ok; ++i) {
-        const int st = i & 1, use = i >> 1;
-        const bool second = i >= c.own_chunks;
-        const int j = second ? i - c.own_chunks : i;
-        const int t = t0 + c.row<REV>(j);
+    bool ok = true;
+    for (; i < c.chunks; ++i) {
+        const int st = i % kStages, use = i / kStages, t = t0 + c.row<REV>(i);
         uint8_t *s = c.base + st * L::stage;
-        if (second) {
-            if (j >= 2) ok = c.wait(bEmptyX + st, ((j >> 1) - 1) & 1);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&c.bar[bFullX + st], L::nx * kSub);
-            for (int u = 0; u < L::nx; ++u) tma_load_4d(s + u * kSub, mx, &c.bar[bFullX + st], 64 * u, c.g.h, t, b);
-        }
-        if (use >= 1 && !(ok = c.wait(bEmptyY + st, (use - 1) & 1))) break;
+        if (use > 0 && !(ok = c.wait(bEmptyY + st, (use - 1) & 1) && c.wait(bEmptyZ + st, (use - 1) & 1))) break;
         mbar_arrive_expect_tx(&c.bar[bFullY + st], L::nx * kSub);
-        for (int u = 0; u < L::nx; ++u)
-            tma_load_4d(s + L::off_y + u * kSub, my, &c.bar[bFullY + st], 64 * u, c.g.h, t, b);
-        if (use >= 1 && !(ok = c.wait(bEmptyZ + st, (use - 1) & 1))) {
-            ++i;   // X and Y of this chunk are on their way
-            break;
-        }
+        for (int u = 0; u < L::nx; ++u) tma_load_4d(s + u * kSub, my, &c.bar[bFullY + st], 64 * u, c.g.h, t, b);
         mbar_arrive_expect_tx(&c.bar[bFullZ + st], L::nz * kSub);
         for (int u = 0; u < L::nz; ++u)
             tma_load_4d(s + L::off_z + u * kSub, mz, &c.bar[bFullZ + st], 64 * u, c.g.h, t, b);
     }
     if (ok) return;
-    // A wait ran out: let the copies in flight land (bounded) before the
-    // shared memory goes away. Stage st was last loaded at chunk k.
+    // a wait ran out: the copies in flight land (bounded) before the shared memory goes away
     uint32_t none = 0;
-    for (int k = i > 2 ? i - 2 : 0; k < i + 1 && k < total; ++k) {
-        const int st = k & 1, use = k >> 1, j = k - c.own_chunks;
-        if (j >= 0) mbar_wait(&c.bar[bFullX + st], (j >> 1) & 1, 1u << 14, &none);
-        mbar_wait(&c.bar[bFullY + st], use & 1, 1u << 14, &none);
-        mbar_wait(&c.bar[bFullZ + st], use & 1, 1u << 14, &none);
+    for (int k = i > kStages ? i - kStages : 0; k < i; ++k) {
+        mbar_wait(&c.bar[bFullY + k % kStages], (k / kStages) & 1, 1u << 14, &none);
+        mbar_wait(&c.bar[bFullZ + k % kStages], (k / kStages) & 1, 1u << 14, &none);
     }
 }
 
+template <int DXP, int DZP, bool REV>
+__device__ void mma_role(const Cta &c)
+{
+    using L = Layout<DXP, DZP>;
+    const uint32_t tmem = (uint32_t)uni((int)c.tmem);
+    const uint64_t zmajor = uni(sdesc_sw128(smem_addr(c.base) + L::off_z, kSub, 1024));
+    const int chunks = uni(c.chunks), packed = uni(c.packed);
+    for (int i = 0; i < chunks; ++i) {
+        const int st = i % kStages, live = uni(c.live<REV>(i));
+        const uint64_t z = zmajor + (uint32_t)st * (L::stage >> 4);
+        if (!c.wait_warp(bFullZ + st, (i / kStages) & 1)) break;
+        if (packed && live < kC && !c.wait_warp(bZReady, 0)) break;
+        if (i > 1 && !c.wait_warp(bBFree + (i & 1), ((i >> 1) - 1) & 1)) break;
+        bool ok = true;
+#pragma unroll 1
+        for (int qd = 0; qd < 4; ++qd) {
+            if (!(ok = c.wait_warp(bYReady + qd, i & 1))) break;
+            tc_fence_after();
+            state_mmas<DZP>(tmem + kColB + (i & 1) * 128, tmem + kColY + 48 * qd, z + qd * 256, live - 32 * qd, qd == 0);
+            warp_commit(&c.bar[bYFree + qd]);
+        }
+        if (!ok) break;
+        warp_commit(&c.bar[bBFull + (i & 1)]);
+        warp_commit(&c.bar[bEmptyZ + st]);
+    }
+    warp_commit(&c.bar[bFin]);
+    uint32_t none = 0;
+    mbar_wait(&c.bar[bFin], 0, kTries, &none);
+}
+
+template <int DXP, int DZP, bool REV>
+__device__ __forceinline__ void state_role(const Cta &c, const Params &p)
+{
+    using L = Layout<DXP, DZP>;
+    State<DXP, DZP, REV> e(c, p, 0);
+    const int first_rank = REV ? c.last_rank : 0;
+    e.clear();
+    if (p.init && c.g.rank == first_rank) {
+        // The sequence's own initial state runs on through its first
+        // segment's state. The copy is for the kernel that starts from it: by
+        // then the caller's may hold the final state already.
+        e.load(p.init, 1.f);
+        e.store_part(REV ? 0 : p.P - 1);
+    }
+    for (int i = 0; i <= c.chunks; ++i) {
+        if (i < c.chunks) {
+            const int st = i % kStages, live = c.live<REV>(i);
+            if (!c.wait_warp(bFullY + st, (i / kStages) & 1)) return;
+            if (c.tail(live)) {
+                if (!c.wait_warp(bFullZ + st, (i / kStages) & 1)) return;
+                e.clear_tail(c.base + st * L::stage + L::off_z, live);
+                arrive_warp(&c.bar[bZReady]);
+            }
+            if (i > 0 && !c.wait_warp(bYFree + e.group, (i - 1) & 1)) return;
+            tc_fence_after();
+            if (e.live_rows) e.send_keys(smem_addr(c.base + st * L::stage), c.tmem + kColY + 48 * e.group, live);
+            tmem_wait_st();
+            tc_fence_before();
+            arrive_warp(&c.bar[bYReady + e.group]);
+            arrive_warp(&c.bar[bEmptyY + st]);
+        }
+        if (i > 0) {   // the chunk before, whose MMAs ran meanwhile
+            const int b = (i - 1) & 1;
+            if (!c.wait_warp(bBFull + b, ((i - 1) >> 1) & 1)) return;
+            tc_fence_after();
+            if (e.live_rows) e.update(c.tmem + kColB + 128 * b, c.live<REV>(i - 1));
+            tc_fence_before();
+            arrive_warp(&c.bar[bBFree + b]);
+        }
+    }
+    e.store_part(c.g.rank);
+}
+
+// One CTA per segment that another one follows: its state into the workspace.
+template <int DXP, int DZP, bool REV>
+__global__ void __launch_bounds__(kThreads, 1)
+la_state_kernel(const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz, const Params p)
+{
+    using L = Layout<DXP, DZP>;
+    extern __shared__ uint8_t smem_raw[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    Cta c;
+    const unsigned head = blockIdx.x / (p.P - 1), rank = blockIdx.x - head * (p.P - 1) + (REV ? 1 : 0);
+    c.g = la_segment(p.cu, p.N, p.T, p.H, p.max_T, p.P, kC, head * p.P + rank);
+    if (!c.g.ok) return;    // reported by the kernel that follows
+    c.base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint32_t *slot = setup(c, p, L::off_aux);
+    if (REV ? c.g.rank > c.last_rank : c.g.rank >= c.last_rank) return;   // no segment follows it
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kBars; ++i)
+            mbar_init(&c.bar[i], i >= bYReady && i < bYFree                                           ? 4
+                                 : (i >= bEmptyY && i < bEmptyZ) || (i >= bBFree && i <= bZReady) ? kStateWarps
+                                                                                                  : 1);
+        fence_mbar_init();
+    }
+    const int warp = uni((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+    if (warp == kMmaWarp) tmem_alloc(slot, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    c.tmem = *slot;
+    if (warp < kStateWarps) seg::state_role<DXP, DZP, REV>(c, p);
+    else if (warp == kMmaWarp) seg::mma_role<DXP, DZP, REV>(c);
+    else if (lane == 0) seg::load_role<DXP, DZP, REV>(c, &my, &mz);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) tmem_dealloc(c.tmem, kTmemCols);
+}
+
+}  // namespace seg
+
+// ================================================================== the outputs
+constexpr int kThreads = 896;
+// warps 0-15 weighted keys and state, 16-19 scores, 20-23 output, then one each:
+constexpr int kScoreWarp = 16, kOutWarp = 20, kLoadWarp = 24, kOutMmaWarp = 25, kStateMmaWarp = 26, kStoreWarp = 27;
+constexpr int kOutWarps = 4;
+
+// TMEM columns (lanes = rows of the chunk, or of the state)
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColA = 0;       // A, fp32; its bf16 form overwrites the first half
+constexpr uint32_t kColY = 128;     // w Y of 32 rows, two buffers: three terms of 16 columns each
+constexpr uint32_t kColB = 224;
+constexpr uint32_t kColO = 352;
+
+enum {
+    bFullX, bFullY = bFullX + 2, bFullZ = bFullY + 2, bEmptyX = bFullZ + 2, bEmptyY = bEmptyX + 2,
+    bEmptyZ = bEmptyY + 2, bAFull = bEmptyZ + 2, bAReady, bInterFull, bInterReady, bOutFull, bOutFree, bStaged, bStored,
+    bYReady, bYFree = bYReady + 2, bBFull = bYFree + 2, bBFree, bStateReady, bZReady, bFinOut, bFinState, kBars
+};
+static_assert(kBars * 8 <= kAuxTables, "");
+
+template <int DXP, int DZP> struct Layout {
+    static constexpr int nx = DXP / 64, nz = DZP / 64;
+    static constexpr bool own_stage = DZP > DXP;           // else the output tile goes over X's
+    static constexpr uint32_t stage = (2 * nx + nz) * kSub;
+    static constexpr uint32_t off_y = nx * kSub, off_z = 2 * nx * kSub;
+    static constexpr uint32_t off_e = 2 * stage;           // bf16 state [DXP][DZP]
+    static constexpr uint32_t e_sub = DXP * 128;
+    static constexpr uint32_t off_out = off_e + nz * e_sub;
+    static constexpr uint32_t off_aux = off_out + (own_stage ? nz * kSub : 0);
+    static constexpr uint32_t bytes = off_aux + kAuxBytes + 1024;
+};
+
+// ------------------------------------------------------------------ loads
+template <int DXP, int DZP, bool REV>
+__device__ void load_role(const Cta &c, const CUtensorMap *mx, const CUtensorMap *my, const CUtensorMap *mz)
+{
+    using L = Layout<DXP, DZP>;
+    const int b = c.packed ? 0 : c.g.n, t0 = c.packed ? (int)c.g.row0 : 0;
+    int i = 0;
+    bool ok = true;
+    for (; i < c.chunks; ++i) {
+        const int st = i & 1, t = t0 + c.row<REV>(i);
+        const uint32_t last = ((i >> 1) - 1) & 1;
+        uint8_t *s = c.base + st * L::stage;
+        if (i >= 2 && !(ok = c.wait(bEmptyY + st, last))) break;
+        mbar_arrive_expect_tx(&c.bar[bFullY + st], L::nx * kSub);
+        for (int u = 0; u < L::nx; ++u)
+            tma_load_4d(s + L::off_y + u * kSub, my, &c.bar[bFullY + st], 64 * u, c.g.h, t, b);
+        if (i >= 2 && !(ok = c.wait(bEmptyX + st, last))) break;
+        mbar_arrive_expect_tx(&c.bar[bFullX + st], L::nx * kSub);
+        for (int u = 0; u < L::nx; ++u) tma_load_4d(s + u * kSub, mx, &c.bar[bFullX + st], 64 * u, c.g.h, t, b);
+        if (i >= 2 && !(ok = c.wait(bEmptyZ + st, last))) break;
+        mbar_arrive_expect_tx(&c.bar[bFullZ + st], L::nz * kSub);
+        for (int u = 0; u < L::nz; ++u)
+            tma_load_4d(s + L::off_z + u * kSub, mz, &c.bar[bFullZ + st], 64 * u, c.g.h, t, b);
+    }
+    if (ok) return;
+    // a wait ran out: the copies in flight land (bounded) before the shared
+    // memory goes away; of chunk i, Y and X may be among them
+    uint32_t none = 0;
+    for (int k = i - 2; k <= i; ++k)
+        for (int q = bFullX; q < bEmptyX; q += 2) mbar_wait(&c.bar[q + (k & 1)], (k >> 1) & 1, 1u << 12, &none);
+}
+
 // ------------------------------------------------------------------ MMAs of scores and output
-// The issuing thread's own instructions are on the MMAs' path (an MMA takes
-// about 68 cycles): descriptors are built once and advanced by an addition
-// to their address field, and the loops over a whole chunk are unrolled.
+// Descriptors are built once and advanced by an addition to their address field.
 template <int DXP, int DZP, bool REV>
 __device__ void out_mma_role(const Cta &c)
 {
     using L = Layout<DXP, DZP>;
-    const uint32_t base = smem_addr(c.base), dA = c.tmem + kColA, dO = c.tmem + kColO;
-    const uint64_t kmajor = sdesc_sw128(base, 0, 1024), zmajor = sdesc_sw128(base + L::off_z, kSub, 1024);
-    const uint64_t emajor = sdesc_sw128(base + L::off_e, L::e_sub, 1024);
+    const uint32_t base = (uint32_t)uni((int)smem_addr(c.base)), tmem = (uint32_t)uni((int)c.tmem);
+    const uint32_t dA = tmem + kColA, dO = tmem + kColO;
+    const uint64_t kmajor = uni(sdesc_sw128(base, 0, 1024)), zmajor = uni(sdesc_sw128(base + L::off_z, kSub, 1024));
+    const uint64_t emajor = uni(sdesc_sw128(base + L::off_e, L::e_sub, 1024));
+    const int chunks = uni(c.chunks), has0 = uni(c.has0), packed = uni(c.packed);
     int inter = 0;
-    for (int j = 0; j < c.chunks; ++j) {
-        const int i = c.own_chunks + j, st = i & 1, live = c.live<REV>(j);
+    for (int j = 0; j < chunks; ++j) {
+        const int st = j & 1, live = uni(c.live<REV>(j));
         const uint32_t stage = (uint32_t)st * (L::stage >> 4);
         const uint64_t x = kmajor + stage, y = x + (L::off_y >> 4), z = zmajor + stage;
-        if (!c.wait(bFullX + st, (j >> 1) & 1) || !c.wait(bFullY + st, (i >> 1) & 1)) break;
+        if (!c.wait_warp(bFullX + st, (j >> 1) & 1) || !c.wait_warp(bFullY + st, (j >> 1) & 1)) break;
         // A's columns are free once the last chunk's A Z has completed
-        if (j > 0 && !c.wait(bOutFull, (j - 1) & 1)) break;
+        if (j > 0 && !c.wait_warp(bOutFull, (j - 1) & 1)) break;
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < DXP / 16; ++k)
-            mma_ss(dA, x + ((k >> 2) * (kSub >> 4) + (k & 3) * 2), y + ((k >> 2) * (kSub >> 4) + (k & 3) * 2),
-                   idesc_bf16(kC, kC, false, false), k > 0);
-        mma_commit(&c.bar[bAFull]);
-        mma_commit(&c.bar[bEmptyY + st]);
-        const bool state = c.has0 || j > 0;
-        if (j > 0 && !c.wait(bOutFree, (j - 1) & 1)) break;
+            warp_mma_ss(dA, x + ((k >> 2) * (kSub >> 4) + (k & 3) * 2), y + ((k >> 2) * (kSub >> 4) + (k & 3) * 2),
+                        idesc_bf16(kC, kC, false, false), k > 0);
+        warp_commit(&c.bar[bAFull]);
+        warp_commit(&c.bar[bEmptyY + st]);
+        const bool state = has0 || j > 0;
+        if (j > 0 && !c.wait_warp(bOutFree, (j - 1) & 1)) break;
         if (state) {
-            if (!c.wait(bStateReady, inter & 1)) break;
+            if (!c.wait_warp(bStateReady, inter & 1)) break;
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < DXP / 16; ++k)
-                mma_ss(dO, x + ((k >> 2) * (kSub >> 4) + (k & 3) * 2), emajor + k * 128,
-                       idesc_bf16(kC, DZP, false, true), k > 0);
-            mma_commit(&c.bar[bInterFull]);
+                warp_mma_ss(dO, x + ((k >> 2) * (kSub >> 4) + (k & 3) * 2), emajor + k * 128,
+                            idesc_bf16(kC, DZP, false, true), k > 0);
+            warp_commit(&c.bar[bInterFull]);
         }
-        if (!c.wait(bFullZ + st, (i >> 1) & 1)) break;
-        if (c.packed && live < kC && !c.wait(bZReady, 0)) break;
-        if (state && !c.wait(bInterReady, inter++ & 1)) break;
-        if (!c.wait(bAReady, j & 1)) break;
+        if (!c.wait_warp(bFullZ + st, (j >> 1) & 1)) break;
+        if (packed && live < kC && !c.wait_warp(bZReady, 0)) break;
+        if (state && !c.wait_warp(bInterReady, inter++ & 1)) break;
+        if (!c.wait_warp(bAReady, j & 1)) break;
         tc_fence_after();
-        if (live > kC - 16) {
+        const int steps = (live + 15) / 16;
 #pragma unroll
-            for (int k = 0; k < kC / 16; ++k)
-                mma_ts(dO, dA + k * 8, z + k * 128, idesc_bf16(kC, DZP, false, true), state || k > 0);
-        } else {
-            for (int k = 0; k < (live + 15) / 16; ++k)
-                mma_ts(dO, dA + k * 8, z + k * 128, idesc_bf16(kC, DZP, false, true), state || k > 0);
-        }
-        mma_commit(&c.bar[bOutFull]);
-        mma_commit(&c.bar[bEmptyZ + st]);
+        for (int k = 0; k < kC / 16; ++k)
+            if (k < steps) warp_mma_ts(dO, dA + k * 8, z + k * 128, idesc_bf16(kC, DZP, false, true), state || k > 0);
+        warp_commit(&c.bar[bOutFull]);
+        warp_commit(&c.bar[bEmptyZ + st]);
     }
-    mma_commit(&c.bar[bFinOut]);
+    warp_commit(&c.bar[bFinOut]);
     uint32_t none = 0;
     mbar_wait(&c.bar[bFinOut], 0, kTries, &none);
 }
@@ -287,94 +662,86 @@ template <int DXP, int DZP, bool REV>
 __device__ void state_mma_role(const Cta &c)
 {
     using L = Layout<DXP, DZP>;
-    const uint32_t dB = c.tmem + kColB, aY = c.tmem + kColY;
-    const uint64_t zmajor = sdesc_sw128(smem_addr(c.base) + L::off_z, kSub, 1024);
-    for (int i = 0; i < c.own_chunks + c.updates; ++i) {
-        const bool second = i >= c.own_chunks;
-        const int st = i & 1, live = c.live<REV>(second ? i - c.own_chunks : i);
+    const uint32_t tmem = (uint32_t)uni((int)c.tmem);
+    const uint64_t zmajor = uni(sdesc_sw128(smem_addr(c.base) + L::off_z, kSub, 1024));
+    const int updates = uni(c.updates), packed = uni(c.packed);
+    for (int i = 0; i < updates; ++i) {
+        const int st = i & 1, live = uni(c.live<REV>(i));
         const uint64_t z = zmajor + (uint32_t)st * (L::stage >> 4);
-        if (!c.wait(bFullZ + st, (i >> 1) & 1)) break;
+        if (!c.wait_warp(bFullZ + st, (i >> 1) & 1)) break;
+        if (packed && live < kC && !c.wait_warp(bZReady, 0)) break;
+        if (i > 0 && !c.wait_warp(bBFree, (i - 1) & 1)) break;
         bool ok = true;
-#pragma unroll
+#pragma unroll 1
         for (int qd = 0; qd < 4; ++qd) {
-            // buffer qd & 1 in its (2 i + qd / 2)-th use
-            if (!(ok = c.wait(bYReady + (qd & 1), (qd >> 1) & 1))) break;
-            if (qd == 0 && i > 0 && !(ok = c.wait(bBFree, (i - 1) & 1))) break;
+            // buffer qd & 1 in its use 2 i + qd / 2
+            if (!(ok = c.wait_warp(bYReady + (qd & 1), qd >> 1))) break;
             tc_fence_after();
-            const int rows = live - 32 * qd;
-#pragma unroll
-            for (int term = 2; term >= 0; --term)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    if (rows > 16 * k)
-                        mma_ts(dB, aY + (qd & 1) * 48 + term * 16 + k * 8, z + (2 * qd + k) * 128,
-                               idesc_bf16(kC, DZP, false, true), qd > 0 || term < 2 || k > 0);
-            mma_commit(&c.bar[bYFree + (qd & 1)]);
+            state_mmas<DZP>(tmem + kColB, tmem + kColY + 48 * (qd & 1), z + qd * 256, live - 32 * qd, qd == 0);
+            warp_commit(&c.bar[bYFree + (qd & 1)]);
         }
         if (!ok) break;
-        mma_commit(&c.bar[bBFull]);
-        mma_commit(&c.bar[bEmptyZ + st]);
-        if (!second) mbar_arrive(&c.bar[bEmptyZ + st]);   // the first phase has no A Z
+        warp_commit(&c.bar[bBFull]);
+        warp_commit(&c.bar[bEmptyZ + st]);
     }
-    mma_commit(&c.bar[bFinState]);
+    warp_commit(&c.bar[bFinState]);
     uint32_t none = 0;
     mbar_wait(&c.bar[bFinState], 0, kTries, &none);
 }
 
 // ------------------------------------------------------------------ scores (lane = row of the chunk)
+// Columns in blocks of 16. A warp's 32 rows see the blocks up to its own two
+// (reverse: from its own two on); |r - s| = [distance to the near edge of the
+// block] + [column within it], so that a block takes one power a row and 16
+// that all rows share.
 template <int DXP, int DZP, bool REV>
 __device__ void score_role(const Cta &c)
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = (threadIdx.x >> 5) - kScoreWarp, lane = threadIdx.x & 31, r = 32 * warp + lane;
     const uint32_t tA = c.tmem + ((uint32_t)(32 * warp) << 16) + kColA;
     for (int j = 0; j < c.chunks; ++j) {
         const int live = c.live<REV>(j);
         if (!c.wait_warp(bAFull, j & 1)) return;
         tc_fence_after();
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b) {   // columns 32b .. 32b+31
-            uint32_t u[32];
-            if (REV ? b < warp : b > warp) {
+        for (int b = 0; b < 8; ++b) {
+            uint32_t o[8];
+            const int own = (b >> 1) - warp;             // before, within, past the warp's own rows
+            if (REV ? own < 0 : own > 0) {
 #pragma unroll
-                for (int q = 0; q < 16; ++q) u[q] = 0;
+                for (int q = 0; q < 8; ++q) o[q] = 0;
             } else {
-                tmem_ld32(tA + 32 * b, u);
-                // |r - s| = [distance to the near edge of the column block] + [column within it]
-                float4 pq[2];
-                const float wr =
-                    b == warp ? 1.f : lds(c.pw + 4 * (REV ? 32 * (b - warp) - lane : 32 * (warp - b) + lane - 31));
+                uint32_t u[16];
+                tmem_ld16(tA + 16 * b, u);
                 tmem_wait_ld();
-                if (b == warp) {
+                float f[16];
+                if (own == 0) {
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) {
-                        const int far = REV ? q - lane : lane - q;
+                    for (int q = 0; q < 16; ++q) {
+                        const int far = REV ? 16 * b + q - r : r - 16 * b - q;
                         const float w = lds(c.pw + 4 * (far >= 0 ? far : 0));
-                        u[q] = far >= 0 ? __float_as_uint(__uint_as_float(u[q]) * w) : 0u;
+                        f[q] = far >= 0 ? __uint_as_float(u[q]) * w : 0.f;
                     }
                 } else {
+                    const float wr = lds(c.pw + 4 * (REV ? 16 * b - r : r - 16 * b - 15));
 #pragma unroll
-                    for (int q = 0; q < 32; q += 8) {
-                        pq[0] = lds4((REV ? c.pw : c.pr) + 4 * q);
-                        pq[1] = lds4((REV ? c.pw : c.pr) + 4 * q + 16);
-                        const float w[8] = {pq[0].x, pq[0].y, pq[0].z, pq[0].w, pq[1].x, pq[1].y, pq[1].z, pq[1].w};
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            u[q + e] = __float_as_uint(__uint_as_float(u[q + e]) * (wr * w[e]));
+                    for (int q = 0; q < 16; q += 4) {
+                        const float4 w = lds4((REV ? c.pw : c.pr) + 4 * q);
+                        f[q] = __uint_as_float(u[q]) * (wr * w.x);
+                        f[q + 1] = __uint_as_float(u[q + 1]) * (wr * w.y);
+                        f[q + 2] = __uint_as_float(u[q + 2]) * (wr * w.z);
+                        f[q + 3] = __uint_as_float(u[q + 3]) * (wr * w.w);
                     }
                 }
                 if (REV && live < kC) {   // columns past the sequence are on the seen side here
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) u[q] = 32 * b + q < live ? u[q] : 0u;
+                    for (int q = 0; q < 16; ++q) f[q] = 16 * b + q < live ? f[q] : 0.f;
                 }
 #pragma unroll
-                for (int q = 0; q < 16; ++q)
-                    u[q] = pack_bf16x2(__uint_as_float(u[2 * q]), __uint_as_float(u[2 * q + 1]));
+                for (int q = 0; q < 8; ++q) o[q] = pack_bf16x2(f[2 * q], f[2 * q + 1]);
             }
-            uint32_t w[16];
-#pragma unroll
-            for (int q = 0; q < 16; ++q) w[q] = u[q];
-            // the fp32 columns that this overwrites (of blocks <= b) have been read
-            tmem_st16(tA + 16 * b, w);
+            // this overwrites fp32 columns of block b / 2, which has been read
+            tmem_st8(tA + 8 * b, o);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -391,20 +758,20 @@ __device__ void out_role(const Cta &c, __nv_bfloat16 *out, int H, int Dz)
     const uint32_t tO = c.tmem + ((uint32_t)(32 * warp) << 16) + kColO;
     int inter = 0;
     for (int j = 0; j < c.chunks; ++j) {
-        const int live = c.live<REV>(j), st = (c.own_chunks + j) & 1;
+        const int live = c.live<REV>(j), st = j & 1;
         if (c.has0 || j > 0) {
             if (!c.wait_warp(bInterFull, inter++ & 1)) return;
             tc_fence_after();
             const int e = REV ? live - 1 - r : r + 1;
             const float wr = e >= 0 ? lds(c.pw + 4 * e) : 0.f;
 #pragma unroll 1
-            for (int b = 0; b < DZP / 32; ++b) {
-                uint32_t u[32];
-                tmem_ld32(tO + 32 * b, u);
+            for (int b = 0; b < DZP / 16; ++b) {
+                uint32_t u[16];
+                tmem_ld16(tO + 16 * b, u);
                 tmem_wait_ld();
 #pragma unroll
-                for (int q = 0; q < 32; ++q) u[q] = __float_as_uint(wr * __uint_as_float(u[q]));
-                tmem_st32(tO + 32 * b, u);
+                for (int q = 0; q < 16; ++q) u[q] = __float_as_uint(wr * __uint_as_float(u[q]));
+                tmem_st16(tO + 16 * b, u);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -413,33 +780,29 @@ __device__ void out_role(const Cta &c, __nv_bfloat16 *out, int H, int Dz)
         if (!c.wait_warp(bOutFull, j & 1)) return;
         tc_fence_after();
         if (L::own_stage && j > 0 && !c.wait_warp(bStored, (j - 1) & 1)) return;
-        const uint32_t tile = smem_addr(c.base) + (L::own_stage ? L::off_out : st * L::stage);
+        uint8_t *tile = c.base + (L::own_stage ? L::off_out : st * L::stage);
 #pragma unroll 1
-        for (int b = 0; b < DZP / 32; ++b) {
-            uint32_t u[32];
-            tmem_ld32(tO + 32 * b, u);
+        for (int b = 0; b < DZP / 16; ++b) {
+            uint32_t u[16], v[8];
+            tmem_ld16(tO + 16 * b, u);
             tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[e] = pack_bf16x2(__uint_as_float(u[8 * q + 2 * e]), __uint_as_float(u[8 * q + 2 * e + 1]));
-                sts4(tile + (b >> 1) * kSub + sw128_offset(r, (b & 1) * 4 + q), v[0], v[1], v[2], v[3]);
-            }
+            for (int q = 0; q < 8; ++q) v[q] = pack_bf16x2(__uint_as_float(u[2 * q]), __uint_as_float(u[2 * q + 1]));
+            const uint32_t t = smem_addr(tile) + (b >> 2) * kSub;
+            sts4(t + sw128_offset(r, (b & 3) * 2), v[0], v[1], v[2], v[3]);
+            sts4(t + sw128_offset(r, (b & 3) * 2 + 1), v[4], v[5], v[6], v[7]);
         }
         tc_fence_before();
         arrive_warp(&c.bar[bOutFree]);
-        if (c.packed && live < kC) {
-            // the last rows of a packed sequence: no TMA store, which would
-            // run on into the next sequence; each warp writes its own rows
-            const uint8_t *t = c.base + (L::own_stage ? L::off_out : st * L::stage);
+        if (c.tail(live)) {
+            // no TMA store, which would run on into the next sequence: each
+            // warp writes its own rows
             const int per = Dz / 8;
             for (int q = lane; q < 32 * per; q += 32) {
                 const int rr = 32 * warp + q / per, ch = q % per;
                 if (rr < live)
                     *(uint4 *)(out + ((c.g.row0 + c.row<REV>(j) + rr) * H + c.g.h) * Dz + ch * 8) =
-                        *(const uint4 *)(t + (ch >> 3) * kSub + sw128_offset(rr, ch & 7));
+                        *(const uint4 *)(tile + (ch >> 3) * kSub + sw128_offset(rr, ch & 7));
             }
         }
         fence_proxy_async_smem();
@@ -453,10 +816,10 @@ __device__ void store_role(const Cta &c, const CUtensorMap *mo)
     using L = Layout<DXP, DZP>;
     const int b = c.packed ? 0 : c.g.n, t0 = c.packed ? (int)c.g.row0 : 0;
     for (int j = 0; j < c.chunks; ++j) {
-        const int st = (c.own_chunks + j) & 1;
+        const int st = j & 1;
         if (!c.wait(bStaged, j & 1)) break;
         const uint8_t *tile = c.base + (L::own_stage ? L::off_out : st * L::stage);
-        if (!(c.packed && c.live<REV>(j) < kC)) {
+        if (!c.tail(c.live<REV>(j))) {
             for (int u = 0; u < L::nz; ++u) tma_store_4d(mo, tile + u * kSub, 64 * u, c.g.h, t0 + c.row<REV>(j), b);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -467,268 +830,70 @@ __device__ void store_role(const Cta &c, const CUtensorMap *mo)
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-// ------------------------------------------------------------------ weighted keys and state (lane = row of the state)
+// ------------------------------------------------------------------ weighted keys and state
 template <int DXP, int DZP, bool REV>
-struct StateRole {
+__device__ __forceinline__ void state_role(const Cta &c, const Params &p)
+{
     using L = Layout<DXP, DZP>;
-    static constexpr int kN = DZP / 2;       // state columns of a thread
-    const Cta &c;
-    const Params &p;
-    int warp, lane, quarter, side, dx, dz0;
-    bool live_rows;                          // this warp's rows are within DXP
-    size_t head;
-    float s[kN];
-
-    __device__ __forceinline__ StateRole(const Cta &c_, const Params &p_) : c(c_), p(p_)
-    {
-        warp = (threadIdx.x >> 5) - kStateWarp;
-        lane = threadIdx.x & 31;
-        quarter = warp & 3;
-        side = warp >> 2;
-        dx = 32 * quarter + lane;
-        dz0 = side * kN;
-        live_rows = 32 * quarter < DXP;
-        head = (size_t)c.g.n * p.H + c.g.h;
+    State<DXP, DZP, REV> e(c, p, 0);
+    const float ld = p.log_decay[c.g.h];
+    const int first_rank = REV ? c.last_rank : 0;
+    e.clear();
+    // the state entering the segment; the segments' own states are of the
+    // launch before this one
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (c.last_rank == 0 || c.chunks == 0) {
+        if (p.init) e.load(p.init, 1.f);
+    } else if (c.g.rank == first_rank) {
+        if (p.init) e.add_part(REV ? 0 : p.P - 1, 1.f);
+    } else {
+        const int to = REV ? c.last_rank + 1 : c.g.rank;
+        for (int q = REV ? c.g.rank + 1 : 0; q < to; ++q)
+            e.add_part(q, la_power(ld, REV ? q * c.g.seg - c.g.end : c.g.begin - (q + 1) * c.g.seg));
     }
-
-    // element (dx, dz0 + q) of an [N,H,..] state; every state in global
-    // memory is read and written once per segment
-    __device__ __forceinline__ void load_scaled(const float *src, float w, bool transposed)
-    {
-        if (dx >= p.Dx || dz0 >= p.Dz) return;
-        if (transposed) {
+    int inter = 0;
+    for (int j = 0; j < c.chunks; ++j) {
+        const int st = j & 1, live = c.live<REV>(j);
+        if (c.has0 || j > 0) {
+            // the bf16 copy that the readout multiplies by, once the last one has been read
+            if (inter > 0 && !c.wait_warp(bInterFull, (inter - 1) & 1)) return;
+            ++inter;
+            if (e.live_rows) {
+                constexpr int kN = State<DXP, DZP, REV>::kN;
+                const uint32_t t = smem_addr(c.base) + L::off_e + (e.dz0 >> 6) * L::e_sub;
 #pragma unroll
-            for (int q = 0; q < kN; ++q)
-                if (dz0 + q < p.Dz) s[q] = fmaf(w, __ldcg(src + (size_t)(dz0 + q) * p.Dx + dx), s[q]);
-        } else {
-#pragma unroll
-            for (int q = 0; q < kN; q += 4)
-                if (dz0 + q < p.Dz) {
-                    const float4 v = __ldcg((const float4 *)(src + (size_t)dx * p.Dz + dz0 + q));
-                    s[q] = fmaf(w, v.x, s[q]);
-                    s[q + 1] = fmaf(w, v.y, s[q + 1]);
-                    s[q + 2] = fmaf(w, v.z, s[q + 2]);
-                    s[q + 3] = fmaf(w, v.w, s[q + 3]);
-                }
-        }
-    }
-    __device__ __forceinline__ void store(float *dst, bool transposed) const
-    {
-        if (dx >= p.Dx || dz0 >= p.Dz) return;
-        if (transposed) {
-#pragma unroll
-            for (int q = 0; q < kN; ++q)
-                if (dz0 + q < p.Dz) dst[(size_t)(dz0 + q) * p.Dx + dx] = s[q];
-        } else {
-#pragma unroll
-            for (int q = 0; q < kN; q += 4)
-                if (dz0 + q < p.Dz)
-                    *(float4 *)(dst + (size_t)dx * p.Dz + dz0 + q) = make_float4(s[q], s[q + 1], s[q + 2], s[q + 3]);
-        }
-    }
-    __device__ __forceinline__ void clear()
-    {
-#pragma unroll
-        for (int q = 0; q < kN; ++q) s[q] = 0.f;
-    }
-
-    // the segment's own state, in an order of the threads' own
-    __device__ __forceinline__ void store_part(float *dst) const
-    {
-        float4 *d = (float4 *)dst + warp * 32 + lane;
-#pragma unroll
-        for (int q = 0; q < kN; q += 4)
-            d[(q / 4) * (kStateWarps * 32)] = make_float4(s[q], s[q + 1], s[q + 2], s[q + 3]);
-    }
-    __device__ __forceinline__ void add_part(const float *src, float w)
-    {
-        const float4 *d = (const float4 *)src + warp * 32 + lane;
-#pragma unroll
-        for (int b = 0; b < kN; b += 32) {
-            float4 v[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = __ldcg(d + (b / 4 + q) * (kStateWarps * 32));
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                s[b + 4 * q] = fmaf(w, v[q].x, s[b + 4 * q]);
-                s[b + 4 * q + 1] = fmaf(w, v[q].y, s[b + 4 * q + 1]);
-                s[b + 4 * q + 2] = fmaf(w, v[q].z, s[b + 4 * q + 2]);
-                s[b + 4 * q + 3] = fmaf(w, v[q].w, s[b + 4 * q + 3]);
+                for (int q = 0; q < kN / 8; ++q)
+                    sts4(t + sw128_offset(e.dx, ((e.dz0 & 63) >> 3) + q), pack_bf16x2(e.s[8 * q], e.s[8 * q + 1]),
+                         pack_bf16x2(e.s[8 * q + 2], e.s[8 * q + 3]), pack_bf16x2(e.s[8 * q + 4], e.s[8 * q + 5]),
+                         pack_bf16x2(e.s[8 * q + 6], e.s[8 * q + 7]));
             }
+            fence_proxy_async_smem();
+            arrive_warp(&c.bar[bStateReady]);
         }
-    }
-
-    // quarter qd of w Y (rows 32 qd .. +31; this warp: 16 of them, 32 state
-    // rows), transposed into TMEM buffer qd & 1 as three bf16 terms
-    __device__ __forceinline__ void send_keys(uint32_t sy, int qd, int live)
-    {
-        const int r0 = 32 * qd + 16 * side;
-        float w[4];
-        uint32_t keep[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int r = r0 + 8 * q + 2 * (lane & 3);
-            if (r + 1 < live) {
-                w[2 * q] = lds(c.pw + 4 * (REV ? r + 1 : live - 1 - r));
-                w[2 * q + 1] = lds(c.pw + 4 * (REV ? r + 2 : live - 2 - r));
-                keep[q] = 0xffffffffu;
-            } else {   // rows past the sequence count as zeros
-                w[2 * q] = lds(c.pw + (REV && r < live ? 4 * (r + 1) : 0));
-                w[2 * q + 1] = 0.f;
-                keep[q] = r < live ? 0xffffu : 0u;
-            }
+        if (c.tail(live)) {
+            if (!c.wait_warp(bFullZ + st, (j >> 1) & 1)) return;
+            e.clear_tail(c.base + st * L::stage + L::off_z, live);
+            arrive_warp(&c.bar[bZReady]);
         }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {    // 16 state rows each
-            const int d = 32 * quarter + 16 * x;
-            const uint32_t chunk = ((d & 63) >> 3) + ((lane >> 3) & 1);
-            uint32_t hi[4], mid[4], lo[4];
-            ldmatrix_x4_trans(sy + (d >> 6) * kSub + sw128_offset(r0 + 8 * (lane >> 4) + (lane & 7), chunk), hi[0],
-                              hi[1], hi[2], hi[3]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t pair = hi[q] & keep[q >> 1];
-                const float a = __uint_as_float(pair << 16) * w[2 * (q >> 1)];
-                const float b = __uint_as_float(pair & 0xffff0000u) * w[2 * (q >> 1) + 1];
-                // the top 8 bits of what is left, three times: 24 in all
-                const float a1 = a - __uint_as_float(__float_as_uint(a) & 0xffff0000u);
-                const float b1 = b - __uint_as_float(__float_as_uint(b) & 0xffff0000u);
-                const float a2 = a1 - __uint_as_float(__float_as_uint(a1) & 0xffff0000u);
-                const float b2 = b1 - __uint_as_float(__float_as_uint(b1) & 0xffff0000u);
-                hi[q] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-                mid[q] = __byte_perm(__float_as_uint(a1), __float_as_uint(b1), 0x7632);
-                lo[q] = __byte_perm(__float_as_uint(a2), __float_as_uint(b2), 0x7632);
-            }
-            const uint32_t t = c.tmem + ((uint32_t)d << 16) + kColY + (qd & 1) * 48 + 8 * side;
-            tmem_st_16x8(t, hi);
-            tmem_st_16x8(t + 16, mid);
-            tmem_st_16x8(t + 32, lo);
-        }
-    }
-
-    // Quarter qd of chunk i (chunk j of its phase) into its buffer, once the
-    // MMAs of the buffer's last use have completed. The first quarter also
-    // waits for the chunk's rows.
-    __device__ __forceinline__ bool send(int i, int j, int qd)
-    {
-        const int st = i & 1, live = c.live<REV>(j);
-        if (qd == 0) {
-            if (!c.wait_warp(bFullY + st, (i >> 1) & 1)) return false;
-            if (c.packed && live < kC && !clear_tail(i, live)) return false;
-        }
-        // the buffer's use before this one: 2 i + qd / 2 - 1
-        if ((i > 0 || qd > 1) && !c.wait_warp(bYFree + (qd & 1), (qd >> 1) ^ 1)) return false;
+        if (j >= c.updates) break;   // nothing reads the state after this chunk
+        if (!c.wait_warp(bFullY + st, (j >> 1) & 1)) return;
+        // quarter `group` in buffer group & 1, whose use before this was 2 j + group / 2 - 1
+        if ((j > 0 || e.group > 1) && !c.wait_warp(bYFree + (e.group & 1), (e.group >> 1) ^ 1)) return;
         tc_fence_after();
-        if (live_rows) send_keys(smem_addr(c.base + st * L::stage + L::off_y), qd, live);
+        if (e.live_rows)
+            e.send_keys(smem_addr(c.base + st * L::stage + L::off_y), c.tmem + kColY + 48 * (e.group & 1), live);
         tmem_wait_st();
         tc_fence_before();
-        arrive_warp(&c.bar[bYReady + (qd & 1)]);
-        return true;
-    }
-
-    // Chunk i: its quarters, the next chunk's first quarter (next_j >= 0; it
-    // covers the wait for this one's MMAs), then E <- gamma^R E + B.
-    __device__ __forceinline__ bool chunk(int i, int j, bool first_phase, int next_j)
-    {
-        if (i == 0 && !send(i, j, 0)) return false;
-#pragma unroll 1
-        for (int qd = 1; qd < 4; ++qd)
-            if (!send(i, j, qd)) return false;
-        arrive_warp(&c.bar[bEmptyY + (i & 1)]);
-        if (first_phase && warp == 0 && lane == 0) mbar_arrive(&c.bar[bEmptyY + (i & 1)]);   // there is no X Y^T
-        if (next_j >= 0 && !send(i + 1, next_j, 0)) return false;
-        if (!c.wait_warp(bBFull, i & 1)) return false;
+        arrive_warp(&c.bar[bYReady + (e.group & 1)]);
+        arrive_warp(&c.bar[bEmptyY + st]);
+        if (!c.wait_warp(bBFull, j & 1)) return;
         tc_fence_after();
-        if (live_rows) {
-            const uint32_t pc = c.pc + (c.live<REV>(j) == kC ? 0 : 8);
-            const float wx = lds(pc), wy = lds(pc + 4);
-#pragma unroll
-            for (int b = 0; b < kN / 16; ++b) {
-                uint32_t u[16];
-                tmem_ld16(c.tmem + ((uint32_t)(32 * quarter) << 16) + kColB + dz0 + 16 * b, u);
-                tmem_wait_ld();
-#pragma unroll
-                for (int q = 0; q < 16; ++q)
-                    s[16 * b + q] = fmaf(s[16 * b + q], wx, fmaf(s[16 * b + q], wy, __uint_as_float(u[q])));
-            }
-        }
+        if (e.live_rows) e.update(c.tmem + kColB, live);
         tc_fence_before();
         arrive_warp(&c.bar[bBFree]);
-        return true;
     }
-
-    // The rows of Z past the end of a packed sequence belong to the next one:
-    // they count as zeros (A and w Y are zero there, but zero times NaN is not).
-    __device__ __forceinline__ bool clear_tail(int i, int live)
-    {
-        const int st = i & 1;
-        if (!c.wait_warp(bFullZ + st, (i >> 1) & 1)) return false;
-        uint8_t *z = c.base + st * L::stage + L::off_z;
-        for (int q = warp * 32 + lane; q < (kC - live) * 8 * L::nz; q += kStateWarps * 32) {
-            const int u = q / ((kC - live) * 8), e = q - u * (kC - live) * 8;
-            *(uint4 *)(z + u * kSub + (live + (e >> 3)) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        if (i >= c.own_chunks) arrive_warp(&c.bar[bZReady]);   // for A Z; w Y's own signal follows
-        return true;
-    }
-
-    // the bf16 copy that the readout multiplies by
-    __device__ __forceinline__ void publish()
-    {
-        if (live_rows) {
-            const uint32_t e = smem_addr(c.base) + L::off_e + (DZP == 128 ? side * L::e_sub : 0);
-#pragma unroll
-            for (int q = 0; q < kN / 8; ++q)
-                sts4(e + sw128_offset(dx, (DZP == 128 ? 0 : 4 * side) + q), pack_bf16x2(s[8 * q], s[8 * q + 1]),
-                     pack_bf16x2(s[8 * q + 2], s[8 * q + 3]), pack_bf16x2(s[8 * q + 4], s[8 * q + 5]),
-                     pack_bf16x2(s[8 * q + 6], s[8 * q + 7]));
-        }
-        fence_proxy_async_smem();
-        arrive_warp(&c.bar[bStateReady]);
-    }
-
-    __device__ __forceinline__ void run()
-    {
-        const size_t cells = (size_t)p.Dx * p.Dz, pad = (size_t)kN * kStateWarps * 32;
-        const int last_rank = c.g.len > 0 ? (c.g.len - 1) / c.g.seg : 0;
-        bool ok = true;
-        clear();
-        for (int i = 0; i < c.own_chunks && ok; ++i)
-            ok = chunk(i, i, true, i + 1 < c.own_chunks ? i + 1 : c.updates > 0 ? 0 : -1);
-        if (p.P > 1) {
-            if (c.own_chunks > 0) store_part(p.part + (head * p.P + c.g.rank) * pad);
-            __threadfence();
-            cluster_arrive();
-            cluster_wait();
-            clear();
-        }
-        if (!ok) return;
-        const float ld = p.log_decay[c.g.h];
-        if (p.init)
-            load_scaled(p.init + head * cells, la_power(ld, REV ? c.g.len - c.g.end : c.g.begin), p.state_t);
-        if (c.g.rank <= last_rank) {
-            const int from = REV ? c.g.rank + 1 : 0, to = REV ? last_rank + 1 : c.g.rank;
-            for (int q = from; q < to; ++q)
-                add_part(p.part + (head * p.P + q) * pad,
-                         la_power(ld, REV ? q * c.g.seg - c.g.end : c.g.begin - (q + 1) * c.g.seg));
-        }
-        if (c.has0 && c.chunks > 0) publish();
-        int inter = 0;
-        for (int j = 0; j < c.chunks; ++j) {
-            const int i = c.own_chunks + j, live = c.live<REV>(j);
-            if (j >= c.updates) {
-                // nothing reads the state after this chunk
-                if (c.packed && live < kC && !clear_tail(i, live)) return;
-                break;
-            }
-            if (!chunk(i, j, false, j + 1 < c.updates ? j + 1 : -1)) return;
-            if ((c.has0 || j > 0) && !c.wait_warp(bInterFull, inter++ & 1)) return;   // the last copy has been read
-            if (j + 1 < c.chunks) publish();
-        }
-        if (p.fin && c.g.rank == (REV ? 0 : last_rank)) store(p.fin + head * cells, p.state_t);
-    }
-};
+    if (p.fin && c.g.rank == (REV ? 0 : c.last_rank)) e.store(p.fin);
+}
 
 template <int DXP, int DZP, bool REV>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -740,83 +905,52 @@ la_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
     extern __shared__ uint8_t smem_raw[];
     Cta c;
     c.g = la_segment(p.cu, p.N, p.T, p.H, p.max_T, p.P, kC, blockIdx.x);
-    if (!c.g.ok) {   // the whole cluster sees the same offsets and leaves together
+    if (!c.g.ok) {
         if (threadIdx.x == 0 && c.g.h == 0 && c.g.rank == 0) report_bad_sequence(p.status);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
     c.base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    c.bar = (uint64_t *)(c.base + L::off_aux);
-    float *pw = (float *)(c.base + L::off_aux + 512), *pr = pw + 132;
-    float2 *pc = (float2 *)(pr + 32);
-    uint32_t *slot = (uint32_t *)(pc + 2);
-    c.pw = smem_addr(pw);
-    c.pr = smem_addr(pr);
-    c.pc = smem_addr(pc);
-    c.abort = slot + 1;
-    c.status = p.status;
-    c.packed = p.cu != nullptr;
-    c.chunks = (c.g.end - c.g.begin + kC - 1) / kC;
-    const int last_rank = c.g.len > 0 ? (c.g.len - 1) / c.g.seg : 0;
-    c.own_chunks = p.P > 1 && (REV ? c.g.rank > 0 : c.g.rank < last_rank) ? c.chunks : 0;
-    c.has0 = p.init != nullptr || (REV ? c.g.rank < last_rank : c.g.rank > 0);
-    const bool write_fin = p.fin && c.g.rank == (REV ? 0 : last_rank);
-    c.updates = write_fin || c.chunks == 0 ? c.chunks : c.chunks - 1;
-
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const float ld = p.log_decay[c.g.h];
-    if (threadIdx.x <= kC) pw[threadIdx.x] = la_power(ld, threadIdx.x);
-    else if (threadIdx.x >= 160 && threadIdx.x < 192) pr[threadIdx.x - 160] = la_power(ld, 191 - threadIdx.x);
-    else if (threadIdx.x == 192) pc[0] = la_power2(ld, kC);
-    else if (threadIdx.x == 224) pc[1] = la_power2(ld, c.g.len % kC);
+    uint32_t *slot = setup(c, p, L::off_aux);
+    c.has0 = p.init != nullptr || (REV ? c.g.rank < c.last_rank : c.g.rank > 0);
+    c.updates = c.chunks - (p.fin && c.g.rank == (REV ? 0 : c.last_rank) ? 0 : 1);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBars; ++i) {
             const int n = i == bAReady || i == bInterReady || i == bOutFree || i == bStaged ? kOutWarps
-                          : i == bYReady || i == bYReady + 1 || i == bBFree || i == bStateReady || i == bZReady
-                              ? kStateWarps
-                          : i == bEmptyY || i == bEmptyY + 1 ? kStateWarps + 1
-                          : i == bEmptyZ || i == bEmptyZ + 1 ? 2
-                                                             : 1;
+                          : i == bYReady || i == bYReady + 1                                ? 4
+                          : i == bBFree || i == bStateReady || i == bZReady                 ? kStateWarps
+                          : i == bEmptyY || i == bEmptyY + 1                                ? kStateWarps + 1
+                          : i == bEmptyZ || i == bEmptyZ + 1                                ? 2
+                                                                                            : 1;
             mbar_init(&c.bar[i], n);
         }
-        *c.abort = 0;
         fence_mbar_init();
     }
-    if (warp == kLoadWarp && lane == 0 && c.chunks > 0) {
-        tma_prefetch_desc(&mx);
-        tma_prefetch_desc(&my);
-        tma_prefetch_desc(&mz);
-        tma_prefetch_desc(&mo);
-    }
-    if (warp == 0) tmem_alloc(slot, kTmemCols);
+    const int warp = uni((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+    if (warp == kStateMmaWarp) tmem_alloc(slot, kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     c.tmem = *slot;
 
-    // registers move to the warps that hold the state (kMovedRegs)
-    if (warp >= kStateWarp && warp < kLoadWarp) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp >= kStateWarp && warp < kLoadWarp) {
-        StateRole<DXP, DZP, REV> role(c, p);
-        role.run();
-    } else {
-        if (p.P > 1) cluster_arrive();
-        if (warp < kOutWarp) {
-            score_role<DXP, DZP, REV>(c);
-        } else if (warp < kStateWarp) {
-            out_role<DXP, DZP, REV>(c, out, p.H, p.Dz);
-        } else if (lane == 0) {
-            if (warp == kLoadWarp) load_role<DXP, DZP, REV>(c, &mx, &my, &mz);
-            else if (warp == kOutMmaWarp) out_mma_role<DXP, DZP, REV>(c);
-            else if (warp == kStateMmaWarp) state_mma_role<DXP, DZP, REV>(c);
-            else store_role<DXP, DZP, REV>(c, &mo);
-        }
-        __syncwarp();
-        if (p.P > 1) cluster_wait();
+    if (warp < kScoreWarp) {
+        state_role<DXP, DZP, REV>(c, p);
+    } else if (warp < kOutWarp) {
+        score_role<DXP, DZP, REV>(c);
+    } else if (warp < kLoadWarp) {
+        out_role<DXP, DZP, REV>(c, out, p.H, p.Dz);
+    } else if (warp == kOutMmaWarp) {
+        out_mma_role<DXP, DZP, REV>(c);
+    } else if (warp == kStateMmaWarp) {
+        state_mma_role<DXP, DZP, REV>(c);
+    } else if (lane == 0) {
+        if (warp == kLoadWarp) load_role<DXP, DZP, REV>(c, &mx, &my, &mz);
+        else store_role<DXP, DZP, REV>(c, &mo);
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(c.tmem, kTmemCols);
+    if (warp == kStateMmaWarp) tmem_dealloc(c.tmem, kTmemCols);
 }
 
 bool rows_map(CUtensorMap *map, const void *base, int D, const LaPass &p)
@@ -831,29 +965,33 @@ bool rows_map(CUtensorMap *map, const void *base, int D, const LaPass &p)
 template <int DXP, int DZP, bool REV>
 cudaError_t launch_sized(const LaPass &p, const CUtensorMap (&m)[4])
 {
-    auto kernel = la_tc_kernel<DXP, DZP, REV>;
-    constexpr int smem = (int)Layout<DXP, DZP>::bytes;
-    // the register moves inside the kernel draw on what the launch allots
-    static const bool fits = [&] {
-        cudaFuncAttributes a;
-        return cudaFuncGetAttributes(&a, kernel) == cudaSuccess && a.numRegs * kThreads >= kMovedRegs;
-    }();
-    if (!fits) return cudaErrorLaunchOutOfResources;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
     const Params pr{p.N, p.T, p.H, p.Dx, p.Dz, p.max_T, p.P, p.log_decay, p.init, p.fin, p.part, p.cu, p.status,
                     p.state_t ? 1 : 0};
+    cudaError_t e;
     cudaLaunchConfig_t cfg = {};
+    cfg.stream = p.stream;
+    if (p.P > 1) {
+        auto states = seg::la_state_kernel<DXP, DZP, REV>;
+        cfg.gridDim = dim3((unsigned)((size_t)p.N * p.H * (p.P - 1)));
+        cfg.blockDim = dim3(seg::kThreads);
+        cfg.dynamicSmemBytes = seg::Layout<DXP, DZP>::bytes;
+        e = cudaFuncSetAttribute(states, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+        if (e != cudaSuccess) return e;
+        if ((e = cudaLaunchKernelEx(&cfg, states, m[1], m[2], pr)) != cudaSuccess) return e;
+    }
+    auto kernel = la_tc_kernel<DXP, DZP, REV>;
     cfg.gridDim = dim3((unsigned)((size_t)p.N * p.H * p.P));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = p.stream;
+    cfg.dynamicSmemBytes = Layout<DXP, DZP>::bytes;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    if (e != cudaSuccess) return e;
+    // its CTAs may start, and load their first rows, while the last of the
+    // segments' states are being made
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.P;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = p.P > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], pr, (__nv_bfloat16 *)p.out);
 }
 
@@ -867,11 +1005,27 @@ cudaError_t launch_dir(const LaPass &p, const CUtensorMap (&m)[4])
 
 bool la_tc_supported(int dtype) { return dtype == DP_BF16 && tensor_map_encoder() != nullptr; }
 
-int la_tc_cluster(int N, int H, int max_T)
+// The number of segments with the least time, in units of a chunk's outputs:
+// a chunk's state alone costs about half of one, a CTA's start and end about
+// one and a half, the second launch two more. Dense sequences run in waves of
+// one CTA per SM; packed ones are bounded by the mean load plus one segment.
+int la_tc_segments(int N, int H, int T, int max_T, bool packed, int sms)
 {
-    int P = 1;
-    while (P < kLaMaxCluster && (long long)N * H * P * 2 <= 152 && max_T >= 2 * P * kC) P *= 2;
-    return P;
+    const double chunks = (max_T + kC - 1) / kC, heads = (double)N * H;
+    int best = 1;
+    double least = 0;
+    for (int P = 1; P <= kLaMaxSegments && (P == 1 || P <= chunks); ++P) {
+        const double seg = ceil(chunks / P) * (P > 1 ? 1.5 : 1.0) + 1.5;
+        double t;
+        if (packed) t = ((double)T / kC * H * (P > 1 ? 1.5 : 1.0) + heads * 1.5 * P) / sms + seg;
+        else t = ceil(heads * P / sms) * seg;
+        if (P > 1) t += 2;
+        if (P == 1 || t < least) {
+            best = P;
+            least = t;
+        }
+    }
+    return best;
 }
 
 cudaError_t launch_la_tc(const LaPass &p)
