@@ -54,8 +54,7 @@ struct Params {
 struct Cta {
     uint8_t *base;
     uint64_t *bar;
-    uint32_t pw;                  // shared: gamma^0 .. gamma^128
-    uint32_t pr;                  // shared: gamma^15 .. gamma^0
+    uint32_t powers;              // shared: the powers of gamma (see setup)
     uint32_t pc;                  // shared: gamma^128, gamma^(rows of the ragged chunk), as two fp32 each
     volatile uint32_t *abort;
     uint32_t *status;
@@ -94,18 +93,31 @@ struct Cta {
     __device__ __forceinline__ bool tail(int rows) const { return packed && rows < kC; }
 };
 
-constexpr uint32_t kAuxBytes = 2048, kAuxTables = 512;   // barriers, then the decay tables
+// Shared memory outside the tiles: barriers, then the tables.
+constexpr uint32_t kAuxBytes = 3072, kAuxTables = 320;
+// The powers of gamma in the order in which a row of the scores meets them
+// along its columns: gamma^128 .. gamma^0 and then zeros forward, 32 zeros and
+// then gamma^0 .. gamma^128 reverse. Four copies, each shifted by one more
+// entry, so that a thread reads any run of them in aligned 16-byte pieces.
+constexpr int kPowers = 164;
+
+template <bool REV> __device__ __forceinline__ uint32_t power_at(uint32_t powers, int n)
+{
+    return powers + 4 * (REV ? 32 + n : 128 - n);
+}
 
 // Tables, barriers' shared memory and the segment; called by every thread
-// before the first barrier. Returns the TMEM address slot.
-__device__ __forceinline__ uint32_t *setup(Cta &c, const Params &p, uint32_t off_aux)
+// before the first barrier. The tiles follow the auxiliary block, at a
+// multiple of 1024 bytes. Returns the TMEM address slot.
+template <bool REV>
+__device__ __forceinline__ uint32_t *setup(Cta &c, const Params &p, uint8_t *smem)
 {
-    c.bar = (uint64_t *)(c.base + off_aux);
-    float *pw = (float *)(c.base + off_aux + kAuxTables), *pr = pw + 132;
-    float2 *pc = (float2 *)(pr + 16);
+    c.base = smem + kAuxBytes;
+    c.bar = (uint64_t *)smem;
+    float *powers = (float *)(smem + kAuxTables);
+    float2 *pc = (float2 *)(powers + 4 * kPowers);
     uint32_t *slot = (uint32_t *)(pc + 2);
-    c.pw = smem_addr(pw);
-    c.pr = smem_addr(pr);
+    c.powers = smem_addr(powers);
     c.pc = smem_addr(pc);
     c.abort = slot + 1;
     c.status = p.status;
@@ -113,12 +125,32 @@ __device__ __forceinline__ uint32_t *setup(Cta &c, const Params &p, uint32_t off
     c.chunks = (c.g.end - c.g.begin + kC - 1) / kC;
     c.last_rank = c.g.len > 0 ? (c.g.len - 1) / c.g.seg : 0;
     const float ld = p.log_decay[c.g.h];
-    if (threadIdx.x <= kC) pw[threadIdx.x] = la_power(ld, threadIdx.x);
-    else if (threadIdx.x >= 160 && threadIdx.x < 176) pr[threadIdx.x - 160] = la_power(ld, 175 - threadIdx.x);
-    else if (threadIdx.x == 192) pc[0] = la_power2(ld, kC);
-    else if (threadIdx.x == 224) pc[1] = la_power2(ld, c.g.len % kC);
+    if (threadIdx.x < kPowers) {
+        const int n = REV ? (int)threadIdx.x - 32 : 128 - (int)threadIdx.x;
+        const float w = n >= 0 && n <= kC ? la_power(ld, n) : 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if ((int)threadIdx.x >= k) powers[k * kPowers + threadIdx.x - k] = w;
+    } else if (threadIdx.x < kPowers + 3) {   // past the last entry of the shifted copies
+        for (int k = threadIdx.x - kPowers + 1; k < 4; ++k)
+            powers[k * kPowers + threadIdx.x - k] = 0.f;
+    } else if (threadIdx.x == 192) {
+        pc[0] = la_power2(ld, kC);
+    } else if (threadIdx.x == 224) {
+        pc[1] = la_power2(ld, c.g.len % kC);
+    }
     if (threadIdx.x == 0) *c.abort = 0;
     return slot;
+}
+
+// The swizzled tiles need their alignment; dynamic shared memory has it as
+// declared. Should it not, the call reports an inconsistency and does nothing.
+__device__ __forceinline__ bool misplaced(const Cta &c)
+{
+    if ((smem_addr(c.base) & 1023u) == 0) return false;
+    if (threadIdx.x == 0 && c.status) atomicCAS(c.status, 0u, (uint32_t)kDevBadState);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return true;
 }
 
 // ------------------------------------------------------------------ instructions
@@ -156,12 +188,12 @@ __device__ __forceinline__ void warp_commit(uint64_t *bar)
         : "memory");
 }
 
-// 16 lanes x 16 columns: register 2j holds lane t/4, column 4j + t%4,
+// 16 lanes x 8 columns: register 2j holds lane t/4, column 4j + t%4,
 // register 2j+1 the lane 8 above it
-__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t (&r)[8])
+__device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t (&r)[4])
 {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
                  : "memory");
 }
 // 32 lanes x 8 columns
@@ -170,6 +202,39 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
+}
+
+// two fp32 at once
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void unpair(uint64_t d, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair_u(uint32_t a, uint32_t b) { return pair(__uint_as_float(a), __uint_as_float(b)); }
+// a bf16 pair as two fp32, and back with rounding
+__device__ __forceinline__ uint64_t widen(uint32_t v) { return pair_u(v << 16, v & 0xffff0000u); }
+__device__ __forceinline__ uint32_t narrow(uint64_t v)
+{
+    float a, b;
+    unpair(v, a, b);
+    return pack_bf16x2(a, b);
 }
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d)
@@ -292,50 +357,53 @@ struct State {
         for (int q = 0; q < kN; ++q) s[q] = 0.f;
     }
 
-    // Quarter `group` of w Y (32 rows by this warp's 32 state rows) from the
-    // tile at sy, transposed into the TMEM columns at `col` as three bf16
-    // terms of 16 columns each.
-    __device__ __forceinline__ void send_keys(uint32_t sy, uint32_t col, int live) const
+    // Rows r0 .. r0+15 of w Y (this warp: its 32 state rows) from the tile at
+    // sy, transposed into 8 TMEM columns at `col` and at each of the next two
+    // multiples of 16 after it: three bf16 terms.
+    __device__ __forceinline__ void send_keys(uint32_t sy, uint32_t col, int r0, int live) const
     {
-        const int first = 32 * group + 2 * (lane & 3);
-        float w[8];
+        const int first = r0 + 2 * (lane & 3);
+        uint64_t w[2];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const int r = first + 8 * (q >> 1) + (q & 1);
-            w[q] = lds(c.pw + 4 * (REV ? r + 1 : r < live ? live - 1 - r : 0));
+        for (int q = 0; q < 2; ++q) {
+            const int r = first + 8 * q;
+            const float w0 = lds(power_at<REV>(c.powers, REV ? r + 1 : r < live ? live - 1 - r : 0));
+            const float w1 = lds(power_at<REV>(c.powers, REV ? r + 2 : r + 1 < live ? live - 2 - r : 0));
+            w[q] = pair(w0, w1);
         }
         // 8 x 8 blocks: two along the rows by two along the state rows
-        const uint32_t row = sy + (quarter >> 1) * kSub + (32 * group + 8 * (lane >> 4) + (lane & 7)) * 128;
+        const uint32_t row = sy + (quarter >> 1) * kSub + (r0 + 8 * (lane >> 4) + (lane & 7)) * 128;
         const uint32_t piece = (uint32_t)((quarter & 1) * 4 + ((lane >> 3) & 1)), flip = lane & 7;
-#pragma unroll 1
-        for (int x = 0; x < 2; ++x) {    // 16 state rows each
-            uint32_t hi[8], mid[8], lo[8];
-            ldmatrix_x4_trans(row + (((piece + 2 * x) ^ flip) << 4), hi[0], hi[1], hi[2], hi[3]);
-            ldmatrix_x4_trans(row + 2048 + (((piece + 2 * x) ^ flip) << 4), hi[4], hi[5], hi[6], hi[7]);
-            if (live < kC) {   // rows past the sequence count as zeros
+        uint32_t y[2][4];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const int r = first + 8 * (q >> 1);
-                    hi[q] &= (r < live ? 0xffffu : 0u) | (r + 1 < live ? 0xffff0000u : 0u);
-                }
+        for (int x = 0; x < 2; ++x)    // 16 state rows each
+            ldmatrix_x4_trans(row + (((piece + 2 * x) ^ flip) << 4), y[x][0], y[x][1], y[x][2], y[x][3]);
+        if (live < kC) {   // rows past the sequence count as zeros
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int r = first + 8 * (q >> 1);
+                const uint32_t keep = (r < live ? 0xffffu : 0u) | (r + 1 < live ? 0xffff0000u : 0u);
+                y[0][q] &= keep;
+                y[1][q] &= keep;
             }
+        }
+        const uint64_t minus = pair(-1.f, -1.f);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float a = __uint_as_float(hi[q] << 16) * w[2 * (q >> 1)];
-                const float b = __uint_as_float(hi[q] & 0xffff0000u) * w[2 * (q >> 1) + 1];
-                // the top 8 bits of what is left, three times: 24 in all
-                const float a1 = a - __uint_as_float(__float_as_uint(a) & 0xffff0000u);
-                const float b1 = b - __uint_as_float(__float_as_uint(b) & 0xffff0000u);
-                const float a2 = a1 - __uint_as_float(__float_as_uint(a1) & 0xffff0000u);
-                const float b2 = b1 - __uint_as_float(__float_as_uint(b1) & 0xffff0000u);
-                hi[q] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-                mid[q] = __byte_perm(__float_as_uint(a1), __float_as_uint(b1), 0x7632);
-                lo[q] = __byte_perm(__float_as_uint(a2), __float_as_uint(b2), 0x7632);
+        for (int x = 0; x < 2; ++x) {
+            uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                // 8 bits at a time: what is left after two roundings fits the third
+                const uint64_t v = mul2(widen(y[x][q]), w[q >> 1]);
+                hi[q] = narrow(v);
+                const uint64_t v1 = fma2(widen(hi[q]), minus, v);
+                mid[q] = narrow(v1);
+                lo[q] = narrow(fma2(widen(mid[q]), minus, v1));
             }
             const uint32_t t = col + ((uint32_t)(32 * quarter + 16 * x) << 16);
-            tmem_st_16x16(t, hi);
-            tmem_st_16x16(t + 16, mid);
-            tmem_st_16x16(t + 32, lo);
+            tmem_st_16x8(t, hi);
+            tmem_st_16x8(t + 16, mid);
+            tmem_st_16x8(t + 32, lo);
         }
     }
 
@@ -343,15 +411,18 @@ struct State {
     __device__ __forceinline__ void update(uint32_t col, int live)
     {
         const uint32_t pc = c.pc + (live == kC ? 0 : 8);
-        const float wx = lds(pc), wy = lds(pc + 4);
+        const float x = lds(pc), y = lds(pc + 4);
+        const uint64_t wx = pair(x, x), wy = pair(y, y);
 #pragma unroll
         for (int b = 0; b < kN / 16; ++b) {
             uint32_t u[16];
             tmem_ld16(col + ((uint32_t)(32 * quarter) << 16) + dz0 + 16 * b, u);
             tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
-                s[16 * b + q] = fmaf(s[16 * b + q], wx, fmaf(s[16 * b + q], wy, __uint_as_float(u[q])));
+            for (int q = 0; q < 16; q += 2) {
+                const uint64_t v = pair(s[16 * b + q], s[16 * b + q + 1]);
+                unpair(fma2(v, wx, fma2(v, wy, pair_u(u[q], u[q + 1]))), s[16 * b + q], s[16 * b + q + 1]);
+            }
         }
     }
 
@@ -386,18 +457,18 @@ namespace seg {
 
 constexpr int kThreads = 576;            // 16 state warps, loads, MMAs
 constexpr int kLoadWarp = 16, kMmaWarp = 17, kStages = 3;
-constexpr uint32_t kColB = 0, kColY = 256, kTmemCols = 512;   // two sums; w Y of each quarter
+// TMEM: the chunk's sum, then w Y of each quarter in two buffers (48 columns each)
+constexpr uint32_t kColB = 0, kColY = 128, kTmemCols = 512;
 enum {
     bFullY, bFullZ = bFullY + kStages, bEmptyY = bFullZ + kStages, bEmptyZ = bEmptyY + kStages,
-    bYReady = bEmptyZ + kStages, bYFree = bYReady + 4, bBFull = bYFree + 4, bBFree = bBFull + 2, bZReady = bBFree + 2,
-    bFin, kBars
+    bYReady = bEmptyZ + kStages, bYFree = bYReady + 8, bBFull = bYFree + 8, bBFree, bZReady, bFin, kBars
 };
 static_assert(kBars * 8 <= kAuxTables, "");
 
 template <int DXP, int DZP> struct Layout {
     static constexpr int nx = DXP / 64, nz = DZP / 64;
     static constexpr uint32_t stage = (nx + nz) * kSub, off_z = nx * kSub;
-    static constexpr uint32_t off_aux = kStages * stage, bytes = off_aux + kAuxBytes + 1024;
+    static constexpr uint32_t bytes = kAuxBytes + kStages * stage;
 };
 
 template <int DXP, int DZP, bool REV>
@@ -438,17 +509,18 @@ __device__ void mma_role(const Cta &c)
         const uint64_t z = zmajor + (uint32_t)st * (L::stage >> 4);
         if (!c.wait_warp(bFullZ + st, (i / kStages) & 1)) break;
         if (packed && live < kC && !c.wait_warp(bZReady, 0)) break;
-        if (i > 1 && !c.wait_warp(bBFree + (i & 1), ((i >> 1) - 1) & 1)) break;
+        if (i > 0 && !c.wait_warp(bBFree, (i - 1) & 1)) break;
         bool ok = true;
 #pragma unroll 1
         for (int qd = 0; qd < 4; ++qd) {
-            if (!(ok = c.wait_warp(bYReady + qd, i & 1))) break;
+            const int buf = 2 * qd + (i & 1);
+            if (!(ok = c.wait_warp(bYReady + buf, (i >> 1) & 1))) break;
             tc_fence_after();
-            state_mmas<DZP>(tmem + kColB + (i & 1) * 128, tmem + kColY + 48 * qd, z + qd * 256, live - 32 * qd, qd == 0);
-            warp_commit(&c.bar[bYFree + qd]);
+            state_mmas<DZP>(tmem + kColB, tmem + kColY + 48 * buf, z + qd * 256, live - 32 * qd, qd == 0);
+            warp_commit(&c.bar[bYFree + buf]);
         }
         if (!ok) break;
-        warp_commit(&c.bar[bBFull + (i & 1)]);
+        warp_commit(&c.bar[bBFull]);
         warp_commit(&c.bar[bEmptyZ + st]);
     }
     warp_commit(&c.bar[bFin]);
@@ -479,21 +551,26 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
                 e.clear_tail(c.base + st * L::stage + L::off_z, live);
                 arrive_warp(&c.bar[bZReady]);
             }
-            if (i > 0 && !c.wait_warp(bYFree + e.group, (i - 1) & 1)) return;
+            const int buf = 2 * e.group + (i & 1);
+            if (i > 1 && !c.wait_warp(bYFree + buf, ((i >> 1) - 1) & 1)) return;
             tc_fence_after();
-            if (e.live_rows) e.send_keys(smem_addr(c.base + st * L::stage), c.tmem + kColY + 48 * e.group, live);
+            if (e.live_rows) {
+                const uint32_t sy = smem_addr(c.base + st * L::stage);
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x)
+                    e.send_keys(sy, c.tmem + kColY + 48 * buf + 8 * x, 32 * e.group + 16 * x, live);
+            }
             tmem_wait_st();
             tc_fence_before();
-            arrive_warp(&c.bar[bYReady + e.group]);
+            arrive_warp(&c.bar[bYReady + buf]);
             arrive_warp(&c.bar[bEmptyY + st]);
         }
         if (i > 0) {   // the chunk before, whose MMAs ran meanwhile
-            const int b = (i - 1) & 1;
-            if (!c.wait_warp(bBFull + b, ((i - 1) >> 1) & 1)) return;
+            if (!c.wait_warp(bBFull, (i - 1) & 1)) return;
             tc_fence_after();
-            if (e.live_rows) e.update(c.tmem + kColB + 128 * b, c.live<REV>(i - 1));
+            if (e.live_rows) e.update(c.tmem + kColB, c.live<REV>(i - 1));
             tc_fence_before();
-            arrive_warp(&c.bar[bBFree + b]);
+            arrive_warp(&c.bar[bBFree]);
         }
     }
     e.store_part(c.g.rank);
@@ -505,20 +582,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 la_state_kernel(const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz, const Params p)
 {
     using L = Layout<DXP, DZP>;
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     Cta c;
     const unsigned head = blockIdx.x / (p.P - 1), rank = blockIdx.x - head * (p.P - 1) + (REV ? 1 : 0);
     c.g = la_segment(p.cu, p.N, p.T, p.H, p.max_T, p.P, kC, head * p.P + rank);
     if (!c.g.ok) return;    // reported by the kernel that follows
-    c.base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint32_t *slot = setup(c, p, L::off_aux);
+    uint32_t *slot = setup<REV>(c, p, smem);
+    if (misplaced(c)) return;
     if (REV ? c.g.rank > c.last_rank : c.g.rank >= c.last_rank) return;   // no segment follows it
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBars; ++i)
-            mbar_init(&c.bar[i], i >= bYReady && i < bYFree                                           ? 4
-                                 : (i >= bEmptyY && i < bEmptyZ) || (i >= bBFree && i <= bZReady) ? kStateWarps
-                                                                                                  : 1);
+            mbar_init(&c.bar[i], i >= bYReady && i < bYFree                                      ? 4
+                                 : (i >= bEmptyY && i < bEmptyZ) || i == bBFree || i == bZReady ? kStateWarps
+                                                                                                : 1);
         fence_mbar_init();
     }
     const int warp = uni((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
@@ -566,8 +643,7 @@ template <int DXP, int DZP> struct Layout {
     static constexpr uint32_t off_e = 2 * stage;           // bf16 state [DXP][DZP]
     static constexpr uint32_t e_sub = DXP * 128;
     static constexpr uint32_t off_out = off_e + nz * e_sub;
-    static constexpr uint32_t off_aux = off_out + (own_stage ? nz * kSub : 0);
-    static constexpr uint32_t bytes = off_aux + kAuxBytes + 1024;
+    static constexpr uint32_t bytes = kAuxBytes + off_out + (own_stage ? nz * kSub : 0);
 };
 
 // ------------------------------------------------------------------ loads
@@ -690,15 +766,16 @@ __device__ void state_mma_role(const Cta &c)
 }
 
 // ------------------------------------------------------------------ scores (lane = row of the chunk)
-// Columns in blocks of 16. A warp's 32 rows see the blocks up to its own two
-// (reverse: from its own two on); |r - s| = [distance to the near edge of the
-// block] + [column within it], so that a block takes one power a row and 16
-// that all rows share.
+// Columns in blocks of 16, each multiplied by a run of the powers table. A
+// warp's 32 rows see the blocks up to its own two (reverse: from its own two
+// on).
 template <int DXP, int DZP, bool REV>
 __device__ void score_role(const Cta &c)
 {
     const int warp = (threadIdx.x >> 5) - kScoreWarp, lane = threadIdx.x & 31, r = 32 * warp + lane;
     const uint32_t tA = c.tmem + ((uint32_t)(32 * warp) << 16) + kColA;
+    const int run = REV ? 32 - r : 128 - r;                          // table entry of column 0
+    const uint32_t w0 = c.powers + 4 * ((run & 3) * kPowers + (run & ~3));
     for (int j = 0; j < c.chunks; ++j) {
         const int live = c.live<REV>(j);
         if (!c.wait_warp(bAFull, j & 1)) return;
@@ -713,32 +790,23 @@ __device__ void score_role(const Cta &c)
             } else {
                 uint32_t u[16];
                 tmem_ld16(tA + 16 * b, u);
+                float4 w[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w[q] = lds4(w0 + 64 * b + 16 * q);
                 tmem_wait_ld();
-                float f[16];
-                if (own == 0) {
+                if (own == 0) {   // the unseen side counts as zeros, whatever it holds
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const int far = REV ? 16 * b + q - r : r - 16 * b - q;
-                        const float w = lds(c.pw + 4 * (far >= 0 ? far : 0));
-                        f[q] = far >= 0 ? __uint_as_float(u[q]) * w : 0.f;
-                    }
-                } else {
-                    const float wr = lds(c.pw + 4 * (REV ? 16 * b - r : r - 16 * b - 15));
-#pragma unroll
-                    for (int q = 0; q < 16; q += 4) {
-                        const float4 w = lds4((REV ? c.pw : c.pr) + 4 * q);
-                        f[q] = __uint_as_float(u[q]) * (wr * w.x);
-                        f[q + 1] = __uint_as_float(u[q + 1]) * (wr * w.y);
-                        f[q + 2] = __uint_as_float(u[q + 2]) * (wr * w.z);
-                        f[q + 3] = __uint_as_float(u[q + 3]) * (wr * w.w);
-                    }
+                    for (int q = 0; q < 16; ++q) u[q] = (REV ? 16 * b + q >= r : 16 * b + q <= r) ? u[q] : 0u;
                 }
                 if (REV && live < kC) {   // columns past the sequence are on the seen side here
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) f[q] = 16 * b + q < live ? f[q] : 0.f;
+                    for (int q = 0; q < 16; ++q) u[q] = 16 * b + q < live ? u[q] : 0u;
                 }
 #pragma unroll
-                for (int q = 0; q < 8; ++q) o[q] = pack_bf16x2(f[2 * q], f[2 * q + 1]);
+                for (int q = 0; q < 4; ++q) {
+                    o[2 * q] = narrow(mul2(pair_u(u[4 * q], u[4 * q + 1]), pair(w[q].x, w[q].y)));
+                    o[2 * q + 1] = narrow(mul2(pair_u(u[4 * q + 2], u[4 * q + 3]), pair(w[q].z, w[q].w)));
+                }
             }
             // this overwrites fp32 columns of block b / 2, which has been read
             tmem_st8(tA + 8 * b, o);
@@ -763,15 +831,21 @@ __device__ void out_role(const Cta &c, __nv_bfloat16 *out, int H, int Dz)
             if (!c.wait_warp(bInterFull, inter++ & 1)) return;
             tc_fence_after();
             const int e = REV ? live - 1 - r : r + 1;
-            const float wr = e >= 0 ? lds(c.pw + 4 * e) : 0.f;
+            const float w = e >= 0 ? lds(power_at<REV>(c.powers, e)) : 0.f;
+            const uint64_t ww = pair(w, w);
 #pragma unroll 1
-            for (int b = 0; b < DZP / 16; ++b) {
-                uint32_t u[16];
-                tmem_ld16(tO + 16 * b, u);
+            for (int b = 0; b < DZP / 32; ++b) {
+                uint32_t u[32];
+                tmem_ld32(tO + 32 * b, u);
                 tmem_wait_ld();
 #pragma unroll
-                for (int q = 0; q < 16; ++q) u[q] = __float_as_uint(wr * __uint_as_float(u[q]));
-                tmem_st16(tO + 16 * b, u);
+                for (int q = 0; q < 32; q += 2) {
+                    float x, y;
+                    unpair(mul2(pair_u(u[q], u[q + 1]), ww), x, y);
+                    u[q] = __float_as_uint(x);
+                    u[q + 1] = __float_as_uint(y);
+                }
+                tmem_st32(tO + 32 * b, u);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -782,15 +856,19 @@ __device__ void out_role(const Cta &c, __nv_bfloat16 *out, int H, int Dz)
         if (L::own_stage && j > 0 && !c.wait_warp(bStored, (j - 1) & 1)) return;
         uint8_t *tile = c.base + (L::own_stage ? L::off_out : st * L::stage);
 #pragma unroll 1
-        for (int b = 0; b < DZP / 16; ++b) {
-            uint32_t u[16], v[8];
-            tmem_ld16(tO + 16 * b, u);
+        for (int b = 0; b < DZP / 32; ++b) {
+            uint32_t u[32];
+            tmem_ld32(tO + 32 * b, u);
             tmem_wait_ld();
+            const uint32_t t = smem_addr(tile) + (b >> 1) * kSub;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = pack_bf16x2(__uint_as_float(u[2 * q]), __uint_as_float(u[2 * q + 1]));
-            const uint32_t t = smem_addr(tile) + (b >> 2) * kSub;
-            sts4(t + sw128_offset(r, (b & 3) * 2), v[0], v[1], v[2], v[3]);
-            sts4(t + sw128_offset(r, (b & 3) * 2 + 1), v[4], v[5], v[6], v[7]);
+            for (int q = 0; q < 4; ++q) {
+                uint32_t v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v[k] = pack_bf16x2(__uint_as_float(u[8 * q + 2 * k]), __uint_as_float(u[8 * q + 2 * k + 1]));
+                sts4(t + sw128_offset(r, (b & 1) * 4 + q), v[0], v[1], v[2], v[3]);
+            }
         }
         tc_fence_before();
         arrive_warp(&c.bar[bOutFree]);
@@ -851,7 +929,10 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
         for (int q = REV ? c.g.rank + 1 : 0; q < to; ++q)
             e.add_part(q, la_power(ld, REV ? q * c.g.seg - c.g.end : c.g.begin - (q + 1) * c.g.seg));
     }
-    int inter = 0;
+    // warps 0-7 send quarters 0 and 2 of a chunk's keys, through the first
+    // buffer, warps 8-15 the others
+    const int side = e.group >> 1;
+    int inter = 0, sent = 0;
     for (int j = 0; j < c.chunks; ++j) {
         const int st = j & 1, live = c.live<REV>(j);
         if (c.has0 || j > 0) {
@@ -876,16 +957,22 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
             arrive_warp(&c.bar[bZReady]);
         }
         if (j >= c.updates) break;   // nothing reads the state after this chunk
-        if (!c.wait_warp(bFullY + st, (j >> 1) & 1)) return;
-        // quarter `group` in buffer group & 1, whose use before this was 2 j + group / 2 - 1
-        if ((j > 0 || e.group > 1) && !c.wait_warp(bYFree + (e.group & 1), (e.group >> 1) ^ 1)) return;
-        tc_fence_after();
-        if (e.live_rows)
-            e.send_keys(smem_addr(c.base + st * L::stage + L::off_y), c.tmem + kColY + 48 * (e.group & 1), live);
-        tmem_wait_st();
-        tc_fence_before();
-        arrive_warp(&c.bar[bYReady + (e.group & 1)]);
-        arrive_warp(&c.bar[bEmptyY + st]);
+        // This side's two quarters of the chunk, and the first side's first
+        // one of the next chunk, which covers the wait for this one's MMAs.
+        const int until = 2 * j + (side == 0 && j + 1 < c.updates ? 3 : 2);
+        for (; sent < until; ++sent) {
+            const int i = sent >> 1, si = i & 1, r0 = 32 * (side + 2 * (sent & 1)) + 16 * (e.group & 1);
+            if (!c.wait_warp(bFullY + si, (i >> 1) & 1)) return;
+            if (sent > 0 && !c.wait_warp(bYFree + side, (sent - 1) & 1)) return;
+            tc_fence_after();
+            if (e.live_rows)
+                e.send_keys(smem_addr(c.base + si * L::stage + L::off_y),
+                            c.tmem + kColY + 48 * side + 8 * (e.group & 1), r0, c.live<REV>(i));
+            tmem_wait_st();
+            tc_fence_before();
+            arrive_warp(&c.bar[bYReady + side]);
+            if (sent & 1) arrive_warp(&c.bar[bEmptyY + si]);
+        }
         if (!c.wait_warp(bBFull, j & 1)) return;
         tc_fence_after();
         if (e.live_rows) e.update(c.tmem + kColB, live);
@@ -902,7 +989,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
              __nv_bfloat16 *out)
 {
     using L = Layout<DXP, DZP>;
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     Cta c;
     c.g = la_segment(p.cu, p.N, p.T, p.H, p.max_T, p.P, kC, blockIdx.x);
     if (!c.g.ok) {
@@ -910,14 +997,14 @@ la_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
-    c.base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint32_t *slot = setup(c, p, L::off_aux);
+    uint32_t *slot = setup<REV>(c, p, smem);
+    if (misplaced(c)) return;
     c.has0 = p.init != nullptr || (REV ? c.g.rank < c.last_rank : c.g.rank > 0);
     c.updates = c.chunks - (p.fin && c.g.rank == (REV ? 0 : c.last_rank) ? 0 : 1);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBars; ++i) {
             const int n = i == bAReady || i == bInterReady || i == bOutFree || i == bStaged ? kOutWarps
-                          : i == bYReady || i == bYReady + 1                                ? 4
+                          : i == bYReady || i == bYReady + 1                                ? kStateWarps / 2
                           : i == bBFree || i == bStateReady || i == bZReady                 ? kStateWarps
                           : i == bEmptyY || i == bEmptyY + 1                                ? kStateWarps + 1
                           : i == bEmptyZ || i == bEmptyZ + 1                                ? 2
