@@ -16,9 +16,13 @@
 // Roundings. A and the copy of E that the readout uses are rounded to bf16
 // (2^-9 of each term, as much as the inputs carry). The state itself is an
 // fp32 result that runs on over the whole sequence, so w Y is not rounded:
-// the fp32 product is cut into three bf16 terms (8 bits each, exact), and B
-// is the sum of three MMAs, the small terms first. The MMAs only add within
-// a chunk; the sum over chunks is an fp32 multiply-add in registers.
+// each weight is three bf16 numbers (24 bits), w = h + m + l, and each product
+// four, exact to 2^-27 of it, which packed bf16 multiply-adds give without
+// unpacking:
+//   t0 = [y h],  t1 = y h - t0,  t2 = [y m],  t3 = [y m - t2 + y l]
+// ([.] rounded; t1 and y m - t2 fit 8 bits). B is the sum of four MMAs, the
+// small terms first. The MMAs only add within a chunk; the sum over chunks is
+// an fp32 multiply-add in registers.
 //
 // Where sequences and heads are too few for the SMs, each sequence is cut into
 // P segments: la_state_kernel runs B and E alone over the segments that others
@@ -37,7 +41,9 @@ namespace {
 using namespace sm100;
 
 constexpr int kC = 128;
-constexpr uint32_t kTries = 1u << 22;
+// A wait polls its barrier at most kTries times; each poll may suspend the
+// warp for up to kSuspend ns, so that waiting warps take few issue slots.
+constexpr uint32_t kTries = 1u << 17, kSuspend = 20000;
 constexpr uint32_t kSub = 16384;    // one [128 rows][64 columns] bf16 tile, 128-byte swizzle
 constexpr int kStateWarps = 16;     // four warpgroups: a quarter of a chunk's keys, of the state's columns each
 
@@ -54,7 +60,8 @@ struct Params {
 struct Cta {
     uint8_t *base;
     uint64_t *bar;
-    uint32_t powers;              // shared: the powers of gamma (see setup)
+    uint32_t powers;              // shared: the powers of gamma
+    uint32_t weights;             // shared: the terms of the key weights of a whole chunk, per pair of rows
     uint32_t pc;                  // shared: gamma^128, gamma^(rows of the ragged chunk), as two fp32 each
     volatile uint32_t *abort;
     uint32_t *status;
@@ -68,9 +75,21 @@ struct Cta {
 
     __device__ __forceinline__ bool wait(int b, uint32_t parity) const
     {
-        if (mbar_wait(&bar[b], parity, kTries, abort)) return true;
+        const uint32_t addr = smem_addr(bar) + 8 * b;
+#pragma unroll 1
+        for (uint32_t i = 0; i < kTries; ++i) {
+            uint32_t done;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(done)
+                : "r"(addr), "r"(parity), "r"(kSuspend)
+                : "memory");
+            if (done) return true;
+            if (*abort) break;
+        }
         *abort = 1;
-        if (status) atomicCAS(status, 0u, (uint32_t)kDevTimeout);
         return false;
     }
     // the same for a whole warp, which agrees on the answer
@@ -97,13 +116,23 @@ struct Cta {
 constexpr uint32_t kAuxBytes = 3072, kAuxTables = 320;
 // The powers of gamma in the order in which a row of the scores meets them
 // along its columns: gamma^128 .. gamma^0 and then zeros forward, 32 zeros and
-// then gamma^0 .. gamma^128 reverse. Four copies, each shifted by one more
-// entry, so that a thread reads any run of them in aligned 16-byte pieces.
-constexpr int kPowers = 164;
+// then gamma^0 .. gamma^128 reverse. Two copies, the second shifted by one
+// entry, so that a thread reads any run of them in aligned pairs.
+constexpr int kPowers = 162;
+constexpr int kTerms = 4;           // bf16 terms of a weighted key
 
 template <bool REV> __device__ __forceinline__ uint32_t power_at(uint32_t powers, int n)
 {
     return powers + 4 * (REV ? 32 + n : 128 - n);
+}
+
+// A weight as three bf16 numbers; pairs of weights packed.
+__device__ __forceinline__ void weight_terms(float w0, float w1, uint32_t &h, uint32_t &m, uint32_t &l)
+{
+    h = sm100::pack_bf16x2(w0, w1);
+    const float a = w0 - __uint_as_float(h << 16), b = w1 - __uint_as_float(h & 0xffff0000u);
+    m = sm100::pack_bf16x2(a, b);
+    l = sm100::pack_bf16x2(a - __uint_as_float(m << 16), b - __uint_as_float(m & 0xffff0000u));
 }
 
 // Tables, barriers' shared memory and the segment; called by every thread
@@ -114,9 +143,11 @@ __device__ __forceinline__ uint32_t *setup(Cta &c, const Params &p, uint8_t *sme
 {
     c.base = smem + kAuxBytes;
     c.bar = (uint64_t *)smem;
-    float *powers = (float *)(smem + kAuxTables);
-    float2 *pc = (float2 *)(powers + 4 * kPowers);
+    uint4 *weights = (uint4 *)(smem + kAuxTables);
+    float *powers = (float *)(weights + kC / 2);
+    float2 *pc = (float2 *)(powers + 2 * kPowers);
     uint32_t *slot = (uint32_t *)(pc + 2);
+    c.weights = smem_addr(weights);
     c.powers = smem_addr(powers);
     c.pc = smem_addr(pc);
     c.abort = slot + 1;
@@ -128,16 +159,18 @@ __device__ __forceinline__ uint32_t *setup(Cta &c, const Params &p, uint8_t *sme
     if (threadIdx.x < kPowers) {
         const int n = REV ? (int)threadIdx.x - 32 : 128 - (int)threadIdx.x;
         const float w = n >= 0 && n <= kC ? la_power(ld, n) : 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if ((int)threadIdx.x >= k) powers[k * kPowers + threadIdx.x - k] = w;
-    } else if (threadIdx.x < kPowers + 3) {   // past the last entry of the shifted copies
-        for (int k = threadIdx.x - kPowers + 1; k < 4; ++k)
-            powers[k * kPowers + threadIdx.x - k] = 0.f;
+        powers[threadIdx.x] = w;
+        if (threadIdx.x > 0) powers[kPowers + threadIdx.x - 1] = w;
+        else powers[2 * kPowers - 1] = 0.f;
     } else if (threadIdx.x == 192) {
         pc[0] = la_power2(ld, kC);
     } else if (threadIdx.x == 224) {
         pc[1] = la_power2(ld, c.g.len % kC);
+    } else if (threadIdx.x >= 256 && threadIdx.x < 256 + kC / 2) {
+        const int r = 2 * (threadIdx.x - 256);
+        uint4 w = make_uint4(0, 0, 0, 0);
+        weight_terms(la_power(ld, REV ? r + 1 : kC - 1 - r), la_power(ld, REV ? r + 2 : kC - 2 - r), w.x, w.y, w.z);
+        weights[r / 2] = w;
     }
     if (threadIdx.x == 0) *c.abort = 0;
     return slot;
@@ -196,14 +229,6 @@ __device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t (&r)
                  "r"(r[2]), "r"(r[3])
                  : "memory");
 }
-// 32 lanes x 8 columns
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
 // two fp32 at once
 __device__ __forceinline__ uint64_t pair(float a, float b)
 {
@@ -227,9 +252,21 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
+// two bf16 at once
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
 __device__ __forceinline__ uint64_t pair_u(uint32_t a, uint32_t b) { return pair(__uint_as_float(a), __uint_as_float(b)); }
-// a bf16 pair as two fp32, and back with rounding
-__device__ __forceinline__ uint64_t widen(uint32_t v) { return pair_u(v << 16, v & 0xffff0000u); }
+// two fp32 rounded to a bf16 pair
 __device__ __forceinline__ uint32_t narrow(uint64_t v)
 {
     float a, b;
@@ -253,10 +290,16 @@ __device__ __forceinline__ float lds(uint32_t a)
     asm("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(a));
     return f;
 }
-__device__ __forceinline__ float4 lds4(uint32_t a)
+__device__ __forceinline__ uint64_t lds_pair(uint32_t a)
 {
-    float4 f;
-    asm("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(a));
+    uint64_t f;
+    asm("ld.shared.b64 %0, [%1];" : "=l"(f) : "r"(a));
+    return f;
+}
+__device__ __forceinline__ uint4 lds_u4(uint32_t a)
+{
+    uint4 f;
+    asm("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(f.x), "=r"(f.y), "=r"(f.z), "=r"(f.w) : "r"(a));
     return f;
 }
 __device__ __forceinline__ void sts4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
@@ -358,19 +401,10 @@ struct State {
     }
 
     // Rows r0 .. r0+15 of w Y (this warp: its 32 state rows) from the tile at
-    // sy, transposed into 8 TMEM columns at `col` and at each of the next two
-    // multiples of 16 after it: three bf16 terms.
+    // sy, transposed into 8 TMEM columns at `col` and at each of the next
+    // three multiples of 16 after it: the four terms.
     __device__ __forceinline__ void send_keys(uint32_t sy, uint32_t col, int r0, int live) const
     {
-        const int first = r0 + 2 * (lane & 3);
-        uint64_t w[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int r = first + 8 * q;
-            const float w0 = lds(power_at<REV>(c.powers, REV ? r + 1 : r < live ? live - 1 - r : 0));
-            const float w1 = lds(power_at<REV>(c.powers, REV ? r + 2 : r + 1 < live ? live - 2 - r : 0));
-            w[q] = pair(w0, w1);
-        }
         // 8 x 8 blocks: two along the rows by two along the state rows
         const uint32_t row = sy + (quarter >> 1) * kSub + (r0 + 8 * (lane >> 4) + (lane & 7)) * 128;
         const uint32_t piece = (uint32_t)((quarter & 1) * 4 + ((lane >> 3) & 1)), flip = lane & 7;
@@ -378,32 +412,46 @@ struct State {
 #pragma unroll
         for (int x = 0; x < 2; ++x)    // 16 state rows each
             ldmatrix_x4_trans(row + (((piece + 2 * x) ^ flip) << 4), y[x][0], y[x][1], y[x][2], y[x][3]);
-        if (live < kC) {   // rows past the sequence count as zeros
+        const int first = r0 + 2 * (lane & 3);
+        uint32_t h[2], m[2], l[2];
+        if (live == kC) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int r = first + 8 * (q >> 1);
+            for (int q = 0; q < 2; ++q) {
+                const uint4 w = lds_u4(c.weights + 8 * first + 64 * q);
+                h[q] = w.x;
+                m[q] = w.y;
+                l[q] = w.z;
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int r = first + 8 * q;
+                weight_terms(lds(power_at<REV>(c.powers, REV ? r + 1 : r < live ? live - 1 - r : 0)),
+                             lds(power_at<REV>(c.powers, REV ? r + 2 : r + 1 < live ? live - 2 - r : 0)), h[q], m[q],
+                             l[q]);
+                // rows past the sequence count as zeros
                 const uint32_t keep = (r < live ? 0xffffu : 0u) | (r + 1 < live ? 0xffff0000u : 0u);
-                y[0][q] &= keep;
-                y[1][q] &= keep;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    y[x][2 * q] &= keep;
+                    y[x][2 * q + 1] &= keep;
+                }
             }
         }
-        const uint64_t minus = pair(-1.f, -1.f);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            uint32_t hi[4], mid[4], lo[4];
+            uint32_t t[kTerms][4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                // 8 bits at a time: what is left after two roundings fits the third
-                const uint64_t v = mul2(widen(y[x][q]), w[q >> 1]);
-                hi[q] = narrow(v);
-                const uint64_t v1 = fma2(widen(hi[q]), minus, v);
-                mid[q] = narrow(v1);
-                lo[q] = narrow(fma2(widen(mid[q]), minus, v1));
+                const uint32_t v = y[x][q];
+                t[0][q] = mul_bf16x2(v, h[q >> 1]);
+                t[1][q] = fma_bf16x2(v, h[q >> 1], t[0][q] ^ 0x80008000u);
+                t[2][q] = mul_bf16x2(v, m[q >> 1]);
+                t[3][q] = fma_bf16x2(v, l[q >> 1], fma_bf16x2(v, m[q >> 1], t[2][q] ^ 0x80008000u));
             }
-            const uint32_t t = col + ((uint32_t)(32 * quarter + 16 * x) << 16);
-            tmem_st_16x8(t, hi);
-            tmem_st_16x8(t + 16, mid);
-            tmem_st_16x8(t + 32, lo);
+            const uint32_t to = col + ((uint32_t)(32 * quarter + 16 * x) << 16);
+#pragma unroll
+            for (int k = 0; k < kTerms; ++k) tmem_st_16x8(to + 16 * k, t[k]);
         }
     }
 
@@ -426,10 +474,37 @@ struct State {
         }
     }
 
+    // O's rows (lane = row of the chunk here; this warpgroup's columns) times
+    // gamma^(r'+o), in TMEM
+    __device__ __forceinline__ void scale_rows(uint32_t col, int live) const
+    {
+        const int n = REV ? live - 1 - dx : dx + 1;
+        const float w = n >= 0 ? lds(power_at<REV>(c.powers, n)) : 0.f;
+        const uint64_t ww = pair(w, w);
+        const uint32_t t = col + ((uint32_t)(32 * quarter) << 16) + dz0;
+#pragma unroll
+        for (int b = 0; b < kN / 16; ++b) {
+            uint32_t u[16];
+            tmem_ld16(t + 16 * b, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 16; q += 2) {
+                float x, y;
+                unpair(mul2(pair_u(u[q], u[q + 1]), ww), x, y);
+                u[q] = __float_as_uint(x);
+                u[q + 1] = __float_as_uint(y);
+            }
+            tmem_st16(t + 16 * b, u);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+    }
+
     // The rows of Z past the end of a packed sequence belong to the next one:
     // they count as zeros (A and w Y are zero there, but zero times NaN is not).
     __device__ __forceinline__ void clear_tail(uint8_t *z, int live) const
     {
+#pragma unroll 1
         for (int q = warp * 32 + lane; q < (kC - live) * 8 * (DZP / 64); q += kStateWarps * 32) {
             const int u = q / ((kC - live) * 8), e = q - u * (kC - live) * 8;
             *(uint4 *)(z + u * kSub + (live + (e >> 3)) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -438,18 +513,18 @@ struct State {
     }
 };
 
-// The MMAs of a quarter of B: three terms of 16 columns at aY against the 32
+// The MMAs of a quarter of B: four terms of 16 columns at aY against the 32
 // rows of Z at `z`; `rows` live ones.
 template <int DZP>
 __device__ __forceinline__ void state_mmas(uint32_t dB, uint32_t aY, uint64_t z, int rows, bool first)
 {
 #pragma unroll
-    for (int term = 2; term >= 0; --term)
+    for (int term = kTerms - 1; term >= 0; --term)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             if (rows > 16 * k)
                 warp_mma_ts(dB, aY + term * 16 + k * 8, z + k * 128, idesc_bf16(kC, DZP, false, true),
-                            !first || term < 2 || k > 0);
+                            !first || term < kTerms - 1 || k > 0);
 }
 
 // ================================================================== the segments' states
@@ -457,11 +532,12 @@ namespace seg {
 
 constexpr int kThreads = 576;            // 16 state warps, loads, MMAs
 constexpr int kLoadWarp = 16, kMmaWarp = 17, kStages = 3;
-// TMEM: the chunk's sum, then w Y of each quarter in two buffers (48 columns each)
-constexpr uint32_t kColB = 0, kColY = 128, kTmemCols = 512;
+// TMEM: the sums of two chunks, then w Y of each quarter (64 columns each)
+constexpr uint32_t kColB = 0, kColY = 256, kTmemCols = 512;
 enum {
     bFullY, bFullZ = bFullY + kStages, bEmptyY = bFullZ + kStages, bEmptyZ = bEmptyY + kStages,
-    bYReady = bEmptyZ + kStages, bYFree = bYReady + 8, bBFull = bYFree + 8, bBFree, bZReady, bFin, kBars
+    bYReady = bEmptyZ + kStages, bYFree = bYReady + 4, bBFull = bYFree + 4, bBFree = bBFull + 2, bZReady = bBFree + 2,
+    bFin, kBars
 };
 static_assert(kBars * 8 <= kAuxTables, "");
 
@@ -478,6 +554,7 @@ __device__ void load_role(const Cta &c, const CUtensorMap *my, const CUtensorMap
     const int b = c.packed ? 0 : c.g.n, t0 = c.packed ? (int)c.g.row0 : 0;
     int i = 0;
     bool ok = true;
+#pragma unroll 1
     for (; i < c.chunks; ++i) {
         const int st = i % kStages, use = i / kStages, t = t0 + c.row<REV>(i);
         uint8_t *s = c.base + st * L::stage;
@@ -504,23 +581,23 @@ __device__ void mma_role(const Cta &c)
     const uint32_t tmem = (uint32_t)uni((int)c.tmem);
     const uint64_t zmajor = uni(sdesc_sw128(smem_addr(c.base) + L::off_z, kSub, 1024));
     const int chunks = uni(c.chunks), packed = uni(c.packed);
+#pragma unroll 1
     for (int i = 0; i < chunks; ++i) {
         const int st = i % kStages, live = uni(c.live<REV>(i));
         const uint64_t z = zmajor + (uint32_t)st * (L::stage >> 4);
         if (!c.wait_warp(bFullZ + st, (i / kStages) & 1)) break;
         if (packed && live < kC && !c.wait_warp(bZReady, 0)) break;
-        if (i > 0 && !c.wait_warp(bBFree, (i - 1) & 1)) break;
+        if (i > 1 && !c.wait_warp(bBFree + (i & 1), ((i >> 1) - 1) & 1)) break;
         bool ok = true;
 #pragma unroll 1
         for (int qd = 0; qd < 4; ++qd) {
-            const int buf = 2 * qd + (i & 1);
-            if (!(ok = c.wait_warp(bYReady + buf, (i >> 1) & 1))) break;
+            if (!(ok = c.wait_warp(bYReady + qd, i & 1))) break;
             tc_fence_after();
-            state_mmas<DZP>(tmem + kColB, tmem + kColY + 48 * buf, z + qd * 256, live - 32 * qd, qd == 0);
-            warp_commit(&c.bar[bYFree + buf]);
+            state_mmas<DZP>(tmem + kColB + (i & 1) * 128, tmem + kColY + 64 * qd, z + qd * 256, live - 32 * qd, qd == 0);
+            warp_commit(&c.bar[bYFree + qd]);
         }
         if (!ok) break;
-        warp_commit(&c.bar[bBFull]);
+        warp_commit(&c.bar[bBFull + (i & 1)]);
         warp_commit(&c.bar[bEmptyZ + st]);
     }
     warp_commit(&c.bar[bFin]);
@@ -542,6 +619,7 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
         e.load(p.init, 1.f);
         e.store_part(REV ? 0 : p.P - 1);
     }
+#pragma unroll 1
     for (int i = 0; i <= c.chunks; ++i) {
         if (i < c.chunks) {
             const int st = i % kStages, live = c.live<REV>(i);
@@ -551,26 +629,26 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
                 e.clear_tail(c.base + st * L::stage + L::off_z, live);
                 arrive_warp(&c.bar[bZReady]);
             }
-            const int buf = 2 * e.group + (i & 1);
-            if (i > 1 && !c.wait_warp(bYFree + buf, ((i >> 1) - 1) & 1)) return;
+            if (i > 0 && !c.wait_warp(bYFree + e.group, (i - 1) & 1)) return;
             tc_fence_after();
             if (e.live_rows) {
                 const uint32_t sy = smem_addr(c.base + st * L::stage);
 #pragma unroll 1
                 for (int x = 0; x < 2; ++x)
-                    e.send_keys(sy, c.tmem + kColY + 48 * buf + 8 * x, 32 * e.group + 16 * x, live);
+                    e.send_keys(sy, c.tmem + kColY + 64 * e.group + 8 * x, 32 * e.group + 16 * x, live);
             }
             tmem_wait_st();
             tc_fence_before();
-            arrive_warp(&c.bar[bYReady + buf]);
+            arrive_warp(&c.bar[bYReady + e.group]);
             arrive_warp(&c.bar[bEmptyY + st]);
         }
         if (i > 0) {   // the chunk before, whose MMAs ran meanwhile
-            if (!c.wait_warp(bBFull, (i - 1) & 1)) return;
+            const int b = (i - 1) & 1;
+            if (!c.wait_warp(bBFull + b, ((i - 1) >> 1) & 1)) return;
             tc_fence_after();
-            if (e.live_rows) e.update(c.tmem + kColB, c.live<REV>(i - 1));
+            if (e.live_rows) e.update(c.tmem + kColB + 128 * b, c.live<REV>(i - 1));
             tc_fence_before();
-            arrive_warp(&c.bar[bBFree]);
+            arrive_warp(&c.bar[bBFree + b]);
         }
     }
     e.store_part(c.g.rank);
@@ -592,9 +670,10 @@ la_state_kernel(const __grid_constant__ CUtensorMap my, const __grid_constant__ 
     if (misplaced(c)) return;
     if (REV ? c.g.rank > c.last_rank : c.g.rank >= c.last_rank) return;   // no segment follows it
     if (threadIdx.x == 0) {
+#pragma unroll 1
         for (int i = 0; i < kBars; ++i)
             mbar_init(&c.bar[i], i >= bYReady && i < bYFree                                      ? 4
-                                 : (i >= bEmptyY && i < bEmptyZ) || i == bBFree || i == bZReady ? kStateWarps
+                                 : (i >= bEmptyY && i < bEmptyZ) || (i >= bBFree && i <= bZReady) ? kStateWarps
                                                                                                 : 1);
         fence_mbar_init();
     }
@@ -610,6 +689,7 @@ la_state_kernel(const __grid_constant__ CUtensorMap my, const __grid_constant__ 
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && *c.abort && c.status) atomicCAS(c.status, 0u, (uint32_t)kDevTimeout);
     if (warp == kMmaWarp) tmem_dealloc(c.tmem, kTmemCols);
 }
 
@@ -617,16 +697,17 @@ la_state_kernel(const __grid_constant__ CUtensorMap my, const __grid_constant__ 
 
 // ================================================================== the outputs
 constexpr int kThreads = 896;
-// warps 0-15 weighted keys and state, 16-19 scores, 20-23 output, then one each:
+// warps 0-15 weighted keys and state, 16-19 scores, 20-23 scores and output, then one each:
 constexpr int kScoreWarp = 16, kOutWarp = 20, kLoadWarp = 24, kOutMmaWarp = 25, kStateMmaWarp = 26, kStoreWarp = 27;
 constexpr int kOutWarps = 4;
 
 // TMEM columns (lanes = rows of the chunk, or of the state)
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColA = 0;       // A, fp32; its bf16 form overwrites the first half
-constexpr uint32_t kColY = 128;     // w Y of 32 rows, two buffers: three terms of 16 columns each
-constexpr uint32_t kColB = 224;
-constexpr uint32_t kColO = 352;
+constexpr uint32_t kColA = 0;       // A, fp32; the bf16 forms of its columns 0-63 and 64-127
+constexpr uint32_t kColA2 = 64;     // overwrite the first half of either
+constexpr uint32_t kColY = 128;     // w Y of 32 rows, two buffers of 64 columns
+constexpr uint32_t kColB = 256;
+constexpr uint32_t kColO = 384;
 
 enum {
     bFullX, bFullY = bFullX + 2, bFullZ = bFullY + 2, bEmptyX = bFullZ + 2, bEmptyY = bEmptyX + 2,
@@ -654,6 +735,7 @@ __device__ void load_role(const Cta &c, const CUtensorMap *mx, const CUtensorMap
     const int b = c.packed ? 0 : c.g.n, t0 = c.packed ? (int)c.g.row0 : 0;
     int i = 0;
     bool ok = true;
+#pragma unroll 1
     for (; i < c.chunks; ++i) {
         const int st = i & 1, t = t0 + c.row<REV>(i);
         const uint32_t last = ((i >> 1) - 1) & 1;
@@ -674,6 +756,7 @@ __device__ void load_role(const Cta &c, const CUtensorMap *mx, const CUtensorMap
     // a wait ran out: the copies in flight land (bounded) before the shared
     // memory goes away; of chunk i, Y and X may be among them
     uint32_t none = 0;
+#pragma unroll 1
     for (int k = i - 2; k <= i; ++k)
         for (int q = bFullX; q < bEmptyX; q += 2) mbar_wait(&c.bar[q + (k & 1)], (k >> 1) & 1, 1u << 12, &none);
 }
@@ -690,6 +773,7 @@ __device__ void out_mma_role(const Cta &c)
     const uint64_t emajor = uni(sdesc_sw128(base + L::off_e, L::e_sub, 1024));
     const int chunks = uni(c.chunks), has0 = uni(c.has0), packed = uni(c.packed);
     int inter = 0;
+#pragma unroll 1
     for (int j = 0; j < chunks; ++j) {
         const int st = j & 1, live = uni(c.live<REV>(j));
         const uint32_t stage = (uint32_t)st * (L::stage >> 4);
@@ -723,7 +807,9 @@ __device__ void out_mma_role(const Cta &c)
         const int steps = (live + 15) / 16;
 #pragma unroll
         for (int k = 0; k < kC / 16; ++k)
-            if (k < steps) warp_mma_ts(dO, dA + k * 8, z + k * 128, idesc_bf16(kC, DZP, false, true), state || k > 0);
+            if (k < steps)
+                warp_mma_ts(dO, k < 4 ? dA + k * 8 : tmem + kColA2 + (k - 4) * 8, z + k * 128,
+                            idesc_bf16(kC, DZP, false, true), state || k > 0);
         warp_commit(&c.bar[bOutFull]);
         warp_commit(&c.bar[bEmptyZ + st]);
     }
@@ -741,6 +827,7 @@ __device__ void state_mma_role(const Cta &c)
     const uint32_t tmem = (uint32_t)uni((int)c.tmem);
     const uint64_t zmajor = uni(sdesc_sw128(smem_addr(c.base) + L::off_z, kSub, 1024));
     const int updates = uni(c.updates), packed = uni(c.packed);
+#pragma unroll 1
     for (int i = 0; i < updates; ++i) {
         const int st = i & 1, live = uni(c.live<REV>(i));
         const uint64_t z = zmajor + (uint32_t)st * (L::stage >> 4);
@@ -753,7 +840,7 @@ __device__ void state_mma_role(const Cta &c)
             // buffer qd & 1 in its use 2 i + qd / 2
             if (!(ok = c.wait_warp(bYReady + (qd & 1), qd >> 1))) break;
             tc_fence_after();
-            state_mmas<DZP>(tmem + kColB, tmem + kColY + 48 * (qd & 1), z + qd * 256, live - 32 * qd, qd == 0);
+            state_mmas<DZP>(tmem + kColB, tmem + kColY + 64 * (qd & 1), z + qd * 256, live - 32 * qd, qd == 0);
             warp_commit(&c.bar[bYFree + (qd & 1)]);
         }
         if (!ok) break;
@@ -766,54 +853,58 @@ __device__ void state_mma_role(const Cta &c)
 }
 
 // ------------------------------------------------------------------ scores (lane = row of the chunk)
-// Columns in blocks of 16, each multiplied by a run of the powers table. A
-// warp's 32 rows see the blocks up to its own two (reverse: from its own two
-// on).
-template <int DXP, int DZP, bool REV>
+// Half of the scores' columns (64 half .. +63) in blocks of 32, each multiplied
+// by a run of the powers table, masked, and rounded to bf16. One warpgroup
+// takes each half: TMEM loads take some hundreds of cycles while the MMAs
+// run, so few large ones on many warps. A warp's 32 rows see the blocks up to
+// their own (reverse: from their own on).
+template <bool REV>
+__device__ __forceinline__ void score_half(const Cta &c, int warp, int half, int live)
+{
+    const int lane = threadIdx.x & 31, r = 32 * warp + lane;
+    const uint32_t tA = c.tmem + ((uint32_t)(32 * warp) << 16);
+    const int run = REV ? 32 - r : 128 - r;                          // table entry of column 0
+    const uint32_t w0 = c.powers + 4 * ((run & 1) * kPowers + (run & ~1));
+#pragma unroll 1
+    for (int n = 0; n < 2; ++n) {
+        const int b = 2 * half + n;
+        uint32_t o[16];
+        if (REV ? b < warp : b > warp) {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) o[q] = 0;
+        } else {
+            uint32_t u[32];
+            tmem_ld32(tA + kColA + 32 * b, u);
+            tmem_wait_ld();
+            if (b == warp) {   // the unseen side counts as zeros, whatever it holds
+#pragma unroll
+                for (int q = 0; q < 32; ++q) u[q] = (REV ? q >= lane : q <= lane) ? u[q] : 0u;
+            }
+            if (REV && live < kC) {   // columns past the sequence are on the seen side here
+#pragma unroll
+                for (int q = 0; q < 32; ++q) u[q] = 32 * b + q < live ? u[q] : 0u;
+            }
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                o[q] = narrow(mul2(pair_u(u[2 * q], u[2 * q + 1]), lds_pair(w0 + 128 * b + 8 * q)));
+        }
+        // over fp32 columns that this warp has read
+        tmem_st16(tA + (half ? kColA2 : kColA) + 16 * n, o);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    arrive_warp(&c.bar[bAReady]);
+}
+
+template <bool REV>
 __device__ void score_role(const Cta &c)
 {
-    const int warp = (threadIdx.x >> 5) - kScoreWarp, lane = threadIdx.x & 31, r = 32 * warp + lane;
-    const uint32_t tA = c.tmem + ((uint32_t)(32 * warp) << 16) + kColA;
-    const int run = REV ? 32 - r : 128 - r;                          // table entry of column 0
-    const uint32_t w0 = c.powers + 4 * ((run & 3) * kPowers + (run & ~3));
+    const int warp = (threadIdx.x >> 5) - kScoreWarp;
+#pragma unroll 1
     for (int j = 0; j < c.chunks; ++j) {
-        const int live = c.live<REV>(j);
         if (!c.wait_warp(bAFull, j & 1)) return;
         tc_fence_after();
-#pragma unroll 1
-        for (int b = 0; b < 8; ++b) {
-            uint32_t o[8];
-            const int own = (b >> 1) - warp;             // before, within, past the warp's own rows
-            if (REV ? own < 0 : own > 0) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) o[q] = 0;
-            } else {
-                uint32_t u[16];
-                tmem_ld16(tA + 16 * b, u);
-                float4 w[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) w[q] = lds4(w0 + 64 * b + 16 * q);
-                tmem_wait_ld();
-                if (own == 0) {   // the unseen side counts as zeros, whatever it holds
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) u[q] = (REV ? 16 * b + q >= r : 16 * b + q <= r) ? u[q] : 0u;
-                }
-                if (REV && live < kC) {   // columns past the sequence are on the seen side here
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) u[q] = 16 * b + q < live ? u[q] : 0u;
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    o[2 * q] = narrow(mul2(pair_u(u[4 * q], u[4 * q + 1]), pair(w[q].x, w[q].y)));
-                    o[2 * q + 1] = narrow(mul2(pair_u(u[4 * q + 2], u[4 * q + 3]), pair(w[q].z, w[q].w)));
-                }
-            }
-            // this overwrites fp32 columns of block b / 2, which has been read
-            tmem_st8(tA + 8 * b, o);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        arrive_warp(&c.bar[bAReady]);
+        score_half<REV>(c, warp, 0, c.live<REV>(j));
     }
 }
 
@@ -824,33 +915,12 @@ __device__ void out_role(const Cta &c, __nv_bfloat16 *out, int H, int Dz)
     using L = Layout<DXP, DZP>;
     const int warp = (threadIdx.x >> 5) - kOutWarp, lane = threadIdx.x & 31, r = 32 * warp + lane;
     const uint32_t tO = c.tmem + ((uint32_t)(32 * warp) << 16) + kColO;
-    int inter = 0;
+#pragma unroll 1
     for (int j = 0; j < c.chunks; ++j) {
         const int live = c.live<REV>(j), st = j & 1;
-        if (c.has0 || j > 0) {
-            if (!c.wait_warp(bInterFull, inter++ & 1)) return;
-            tc_fence_after();
-            const int e = REV ? live - 1 - r : r + 1;
-            const float w = e >= 0 ? lds(power_at<REV>(c.powers, e)) : 0.f;
-            const uint64_t ww = pair(w, w);
-#pragma unroll 1
-            for (int b = 0; b < DZP / 32; ++b) {
-                uint32_t u[32];
-                tmem_ld32(tO + 32 * b, u);
-                tmem_wait_ld();
-#pragma unroll
-                for (int q = 0; q < 32; q += 2) {
-                    float x, y;
-                    unpair(mul2(pair_u(u[q], u[q + 1]), ww), x, y);
-                    u[q] = __float_as_uint(x);
-                    u[q + 1] = __float_as_uint(y);
-                }
-                tmem_st32(tO + 32 * b, u);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            arrive_warp(&c.bar[bInterReady]);
-        }
+        if (!c.wait_warp(bAFull, j & 1)) return;
+        tc_fence_after();
+        score_half<REV>(c, warp, 1, live);
         if (!c.wait_warp(bOutFull, j & 1)) return;
         tc_fence_after();
         if (L::own_stage && j > 0 && !c.wait_warp(bStored, (j - 1) & 1)) return;
@@ -876,6 +946,7 @@ __device__ void out_role(const Cta &c, __nv_bfloat16 *out, int H, int Dz)
             // no TMA store, which would run on into the next sequence: each
             // warp writes its own rows
             const int per = Dz / 8;
+#pragma unroll 1
             for (int q = lane; q < 32 * per; q += 32) {
                 const int rr = 32 * warp + q / per, ch = q % per;
                 if (rr < live)
@@ -893,6 +964,7 @@ __device__ void store_role(const Cta &c, const CUtensorMap *mo)
 {
     using L = Layout<DXP, DZP>;
     const int b = c.packed ? 0 : c.g.n, t0 = c.packed ? (int)c.g.row0 : 0;
+#pragma unroll 1
     for (int j = 0; j < c.chunks; ++j) {
         const int st = j & 1;
         if (!c.wait(bStaged, j & 1)) break;
@@ -926,6 +998,7 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
         if (p.init) e.add_part(REV ? 0 : p.P - 1, 1.f);
     } else {
         const int to = REV ? c.last_rank + 1 : c.g.rank;
+#pragma unroll 1
         for (int q = REV ? c.g.rank + 1 : 0; q < to; ++q)
             e.add_part(q, la_power(ld, REV ? q * c.g.seg - c.g.end : c.g.begin - (q + 1) * c.g.seg));
     }
@@ -933,12 +1006,12 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
     // buffer, warps 8-15 the others
     const int side = e.group >> 1;
     int inter = 0, sent = 0;
+#pragma unroll 1
     for (int j = 0; j < c.chunks; ++j) {
         const int st = j & 1, live = c.live<REV>(j);
         if (c.has0 || j > 0) {
-            // the bf16 copy that the readout multiplies by, once the last one has been read
-            if (inter > 0 && !c.wait_warp(bInterFull, (inter - 1) & 1)) return;
-            ++inter;
+            // the bf16 copy that the readout multiplies by (the last one has
+            // been read: its product was scaled below)
             if (e.live_rows) {
                 constexpr int kN = State<DXP, DZP, REV>::kN;
                 const uint32_t t = smem_addr(c.base) + L::off_e + (e.dz0 >> 6) * L::e_sub;
@@ -956,10 +1029,11 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
             e.clear_tail(c.base + st * L::stage + L::off_z, live);
             arrive_warp(&c.bar[bZReady]);
         }
-        if (j >= c.updates) break;   // nothing reads the state after this chunk
-        // This side's two quarters of the chunk, and the first side's first
-        // one of the next chunk, which covers the wait for this one's MMAs.
-        const int until = 2 * j + (side == 0 && j + 1 < c.updates ? 3 : 2);
+        // This side's two quarters of the chunk (none for the last chunk where
+        // nothing reads the state after it), and the first side's first one of
+        // the next chunk, which covers the wait for this one's MMAs.
+        const int until = j >= c.updates ? 0 : 2 * j + (side == 0 && j + 1 < c.updates ? 3 : 2);
+#pragma unroll 1
         for (; sent < until; ++sent) {
             const int i = sent >> 1, si = i & 1, r0 = 32 * (side + 2 * (sent & 1)) + 16 * (e.group & 1);
             if (!c.wait_warp(bFullY + si, (i >> 1) & 1)) return;
@@ -967,12 +1041,19 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
             tc_fence_after();
             if (e.live_rows)
                 e.send_keys(smem_addr(c.base + si * L::stage + L::off_y),
-                            c.tmem + kColY + 48 * side + 8 * (e.group & 1), r0, c.live<REV>(i));
+                            c.tmem + kColY + 64 * side + 8 * (e.group & 1), r0, c.live<REV>(i));
             tmem_wait_st();
             tc_fence_before();
             arrive_warp(&c.bar[bYReady + side]);
             if (sent & 1) arrive_warp(&c.bar[bEmptyY + si]);
         }
+        if (c.has0 || j > 0) {
+            if (!c.wait_warp(bInterFull, inter++ & 1)) return;
+            tc_fence_after();
+            e.scale_rows(c.tmem + kColO, live);
+            arrive_warp(&c.bar[bInterReady]);
+        }
+        if (j >= c.updates) break;
         if (!c.wait_warp(bBFull, j & 1)) return;
         tc_fence_after();
         if (e.live_rows) e.update(c.tmem + kColB, live);
@@ -1002,8 +1083,11 @@ la_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
     c.has0 = p.init != nullptr || (REV ? c.g.rank < c.last_rank : c.g.rank > 0);
     c.updates = c.chunks - (p.fin && c.g.rank == (REV ? 0 : c.last_rank) ? 0 : 1);
     if (threadIdx.x == 0) {
+#pragma unroll 1
         for (int i = 0; i < kBars; ++i) {
-            const int n = i == bAReady || i == bInterReady || i == bOutFree || i == bStaged ? kOutWarps
+            const int n = i == bOutFree || i == bStaged                                     ? kOutWarps
+                          : i == bAReady                                                    ? 2 * kOutWarps
+                          : i == bInterReady                                                ? kStateWarps
                           : i == bYReady || i == bYReady + 1                                ? kStateWarps / 2
                           : i == bBFree || i == bStateReady || i == bZReady                 ? kStateWarps
                           : i == bEmptyY || i == bEmptyY + 1                                ? kStateWarps + 1
@@ -1023,7 +1107,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
     if (warp < kScoreWarp) {
         state_role<DXP, DZP, REV>(c, p);
     } else if (warp < kOutWarp) {
-        score_role<DXP, DZP, REV>(c);
+        score_role<REV>(c);
     } else if (warp < kLoadWarp) {
         out_role<DXP, DZP, REV>(c, out, p.H, p.Dz);
     } else if (warp == kOutMmaWarp) {
@@ -1037,6 +1121,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && *c.abort && c.status) atomicCAS(c.status, 0u, (uint32_t)kDevTimeout);
     if (warp == kStateMmaWarp) tmem_dealloc(c.tmem, kTmemCols);
 }
 
