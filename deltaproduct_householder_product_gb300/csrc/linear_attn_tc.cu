@@ -6,12 +6,20 @@
 // registers, its bf16 copy in shared memory):
 //   A  = X Y^T                 MMA, then gamma^|r-s| and the causal mask in
 //                              fp32, rounded to bf16 into TMEM
-//   O  = X E                   MMA, its rows scaled by gamma^(r'+o) in TMEM
+//   O  = X E                   MMA
 //   O += A Z                   MMA (A from TMEM), rounded to bf16, TMA store
 //   B  = (w Y)^T Z             MMA (w Y from TMEM)
 //   E  = gamma^R E + B         registers
 // B does not depend on E, so the chunks' MMAs do not wait for one another;
 // the one recurrence is the last line.
+//
+// The readout's rows carry gamma^(r'+o) as well. Where gamma^128 is no smaller
+// than 2^-32 (`mild` heads) that factor is taken out of the whole row: A holds
+// gamma^-(column's distance from the chunk's edge) only, O is the plain sum of
+// both products, and the output multiplies its rows; the factors stay within
+// 2^32, so that nothing leaves the range of fp32 that did not before, up to
+// scores times values of 2^95. Stronger decays would overflow there: A holds
+// gamma^|r-s|, and O is scaled in TMEM between the two products.
 //
 // Roundings. A and the copy of E that the readout uses are rounded to bf16
 // (2^-9 of each term, as much as the inputs carry). The state itself is an
@@ -61,6 +69,7 @@ struct Cta {
     uint8_t *base;
     uint64_t *bar;
     uint32_t powers;              // shared: the powers of gamma
+    uint32_t columns;             // shared: a mild head's powers for the scores' columns
     uint32_t weights;             // shared: the terms of the key weights of a whole chunk, per pair of rows
     uint32_t pc;                  // shared: gamma^128, gamma^(rows of the ragged chunk), as two fp32 each
     volatile uint32_t *abort;
@@ -71,6 +80,7 @@ struct Cta {
     int chunks;                   // of this segment
     int updates;                  // of them, those whose rows go into the state
     bool has0;                    // a state enters the segment
+    bool mild;                    // gamma^128 >= 2^-32
     bool packed;
 
     __device__ __forceinline__ bool wait(int b, uint32_t parity) const
@@ -116,9 +126,12 @@ struct Cta {
 constexpr uint32_t kAuxBytes = 3072, kAuxTables = 320;
 // The powers of gamma in the order in which a row of the scores meets them
 // along its columns: gamma^128 .. gamma^0 and then zeros forward, 32 zeros and
-// then gamma^0 .. gamma^128 reverse. Two copies, the second shifted by one
-// entry, so that a thread reads any run of them in aligned pairs.
+// then gamma^0 .. gamma^128 reverse. A second copy, shifted by one entry, lets
+// a thread read any run of them in aligned pairs; for a mild head its place
+// holds the columns' powers instead, gamma^-(s+1) forward and gamma^-(127-s)
+// reverse.
 constexpr int kPowers = 162;
+constexpr float kMildLog = 0.17328680f;   // 32 ln 2 / 128
 constexpr int kTerms = 4;           // bf16 terms of a weighted key
 
 template <bool REV> __device__ __forceinline__ uint32_t power_at(uint32_t powers, int n)
@@ -156,12 +169,20 @@ __device__ __forceinline__ uint32_t *setup(Cta &c, const Params &p, uint8_t *sme
     c.chunks = (c.g.end - c.g.begin + kC - 1) / kC;
     c.last_rank = c.g.len > 0 ? (c.g.len - 1) / c.g.seg : 0;
     const float ld = p.log_decay[c.g.h];
+    c.mild = fabsf(ld) <= kMildLog;
+    c.columns = smem_addr(powers + kPowers);
     if (threadIdx.x < kPowers) {
         const int n = REV ? (int)threadIdx.x - 32 : 128 - (int)threadIdx.x;
         const float w = n >= 0 && n <= kC ? la_power(ld, n) : 0.f;
         powers[threadIdx.x] = w;
-        if (threadIdx.x > 0) powers[kPowers + threadIdx.x - 1] = w;
-        else powers[2 * kPowers - 1] = 0.f;
+        if (c.mild) {
+            if (threadIdx.x < kC)
+                powers[kPowers + threadIdx.x] = expf((REV ? (float)threadIdx.x - 127.f : -1.f - (float)threadIdx.x) * ld);
+        } else if (threadIdx.x > 0) {
+            powers[kPowers + threadIdx.x - 1] = w;
+        } else {
+            powers[2 * kPowers - 1] = 0.f;
+        }
     } else if (threadIdx.x == 192) {
         pc[0] = la_power2(ld, kC);
     } else if (threadIdx.x == 224) {
@@ -772,6 +793,7 @@ __device__ void out_mma_role(const Cta &c)
     const uint64_t kmajor = uni(sdesc_sw128(base, 0, 1024)), zmajor = uni(sdesc_sw128(base + L::off_z, kSub, 1024));
     const uint64_t emajor = uni(sdesc_sw128(base + L::off_e, L::e_sub, 1024));
     const int chunks = uni(c.chunks), has0 = uni(c.has0), packed = uni(c.packed);
+    const int mild = uni(c.mild);
     int inter = 0;
 #pragma unroll 1
     for (int j = 0; j < chunks; ++j) {
@@ -801,7 +823,8 @@ __device__ void out_mma_role(const Cta &c)
         }
         if (!c.wait_warp(bFullZ + st, (j >> 1) & 1)) break;
         if (packed && live < kC && !c.wait_warp(bZReady, 0)) break;
-        if (state && !c.wait_warp(bInterReady, inter++ & 1)) break;
+        if (state && !mild && !c.wait_warp(bInterReady, inter & 1)) break;
+        inter += state;
         if (!c.wait_warp(bAReady, j & 1)) break;
         tc_fence_after();
         const int steps = (live + 15) / 16;
@@ -864,7 +887,7 @@ __device__ __forceinline__ void score_half(const Cta &c, int warp, int half, int
     const int lane = threadIdx.x & 31, r = 32 * warp + lane;
     const uint32_t tA = c.tmem + ((uint32_t)(32 * warp) << 16);
     const int run = REV ? 32 - r : 128 - r;                          // table entry of column 0
-    const uint32_t w0 = c.powers + 4 * ((run & 1) * kPowers + (run & ~1));
+    const uint32_t w0 = c.mild ? c.columns : c.powers + 4 * ((run & 1) * kPowers + (run & ~1));
 #pragma unroll 1
     for (int n = 0; n < 2; ++n) {
         const int b = 2 * half + n;
@@ -915,6 +938,8 @@ __device__ void out_role(const Cta &c, __nv_bfloat16 *out, int H, int Dz)
     using L = Layout<DXP, DZP>;
     const int warp = (threadIdx.x >> 5) - kOutWarp, lane = threadIdx.x & 31, r = 32 * warp + lane;
     const uint32_t tO = c.tmem + ((uint32_t)(32 * warp) << 16) + kColO;
+    const float w = c.mild ? lds(power_at<REV>(c.powers, REV ? 127 - r : r + 1)) : 1.f;
+    const uint64_t ww = pair(w, w);
 #pragma unroll 1
     for (int j = 0; j < c.chunks; ++j) {
         const int live = c.live<REV>(j), st = j & 1;
@@ -935,8 +960,7 @@ __device__ void out_role(const Cta &c, __nv_bfloat16 *out, int H, int Dz)
             for (int q = 0; q < 4; ++q) {
                 uint32_t v[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    v[k] = pack_bf16x2(__uint_as_float(u[8 * q + 2 * k]), __uint_as_float(u[8 * q + 2 * k + 1]));
+                for (int k = 0; k < 4; ++k) v[k] = narrow(mul2(pair_u(u[8 * q + 2 * k], u[8 * q + 2 * k + 1]), ww));
                 sts4(t + sw128_offset(r, (b & 1) * 4 + q), v[0], v[1], v[2], v[3]);
             }
         }
@@ -1011,15 +1035,20 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
         const int st = j & 1, live = c.live<REV>(j);
         if (c.has0 || j > 0) {
             // the bf16 copy that the readout multiplies by (the last one has
-            // been read: its product was scaled below)
+            // been read: its product was waited for below)
             if (e.live_rows) {
                 constexpr int kN = State<DXP, DZP, REV>::kN;
+                // reverse, a mild head's rows count from the end of a whole chunk
+                float f[kN];
+                const float edge = REV && c.mild && live < kC ? expf((float)(live - kC) * ld) : 1.f;
+#pragma unroll
+                for (int q = 0; q < kN; ++q) f[q] = REV ? e.s[q] * edge : e.s[q];
                 const uint32_t t = smem_addr(c.base) + L::off_e + (e.dz0 >> 6) * L::e_sub;
 #pragma unroll
                 for (int q = 0; q < kN / 8; ++q)
-                    sts4(t + sw128_offset(e.dx, ((e.dz0 & 63) >> 3) + q), pack_bf16x2(e.s[8 * q], e.s[8 * q + 1]),
-                         pack_bf16x2(e.s[8 * q + 2], e.s[8 * q + 3]), pack_bf16x2(e.s[8 * q + 4], e.s[8 * q + 5]),
-                         pack_bf16x2(e.s[8 * q + 6], e.s[8 * q + 7]));
+                    sts4(t + sw128_offset(e.dx, ((e.dz0 & 63) >> 3) + q), pack_bf16x2(f[8 * q], f[8 * q + 1]),
+                         pack_bf16x2(f[8 * q + 2], f[8 * q + 3]), pack_bf16x2(f[8 * q + 4], f[8 * q + 5]),
+                         pack_bf16x2(f[8 * q + 6], f[8 * q + 7]));
             }
             fence_proxy_async_smem();
             arrive_warp(&c.bar[bStateReady]);
@@ -1049,9 +1078,11 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
         }
         if (c.has0 || j > 0) {
             if (!c.wait_warp(bInterFull, inter++ & 1)) return;
-            tc_fence_after();
-            e.scale_rows(c.tmem + kColO, live);
-            arrive_warp(&c.bar[bInterReady]);
+            if (!c.mild) {
+                tc_fence_after();
+                e.scale_rows(c.tmem + kColO, live);
+                arrive_warp(&c.bar[bInterReady]);
+            }
         }
         if (j >= c.updates) break;
         if (!c.wait_warp(bBFull, j & 1)) return;
