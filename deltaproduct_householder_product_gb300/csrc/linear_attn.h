@@ -108,15 +108,38 @@ __device__ __forceinline__ float la_power(float log_decay, int n)
     return n == 0 ? 1.f : expf((float)n * log_decay);
 }
 
-// gamma^n as the sum of two fp32 values. The state is multiplied by the same
-// power once per chunk, so a rounding of that power would grow with the
-// number of chunks a head remembers.
+// gamma^n as the sum of two fp32 values, to about 2^-28 of it. The state is
+// multiplied by the same power once per chunk, so an error of that power
+// grows with the number of chunks that a head remembers. In pairs of fp32
+// (the 64-bit unit would take microseconds): n log gamma = k ln 2 + r exactly
+// enough, exp(r / 8) by its series, squared three times, times 2^k.
 __device__ __forceinline__ float2 la_power2(float log_decay, int n)
 {
     if (n == 0) return make_float2(1.f, 0.f);
-    const double w = exp((double)n * (double)log_decay);
-    const float hi = (float)w;
-    return make_float2(hi, isfinite(hi) ? (float)(w - (double)hi) : 0.f);
+    const float m = (float)n, xh = m * log_decay;
+    if (!(xh > -104.f && xh < 88.f)) return make_float2(expf(xh), 0.f);   // 0, overflow, NaN
+    const float xl = fmaf(m, log_decay, -xh);
+    const float k = rintf(xh * 1.44269504f);
+    // ln 2 in two parts; k times the first (16 bits) is exact
+    const float a = fmaf(k, -0.693145751953125f, xh), t = k * 1.42860682e-6f;
+    const float rh = a - t, rl = ((a - rh) - t) + xl - fmaf(k, 1.42860682e-6f, -t);
+    const float u = 0.125f * rh, v = 0.125f * rl;
+    // exp(u + v) = 1 + u + (v + u v + u^2/2 + ..): |u| < 0.044, |v| < 2^-20
+    float q = fmaf(u, 1.f / 720.f, 1.f / 120.f);
+    q = fmaf(u, q, 1.f / 24.f);
+    q = fmaf(u, q, 1.f / 6.f);
+    q = fmaf(u, q, 0.5f);
+    q = fmaf(u * u, q, fmaf(u, v, v));
+    float h = 1.f + u, l = (u - (h - 1.f)) + q;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const float p = h * h;
+        l = fmaf(2.f * h, l, fmaf(l, l, fmaf(h, h, -p)));
+        h = p;
+    }
+    const float s = h + l;
+    l -= s - h;
+    return make_float2(ldexpf(s, (int)k), ldexpf(l, (int)k));
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }

@@ -371,23 +371,64 @@ struct State {
         head = (size_t)c.g.n * p.H + c.g.h;
     }
 
+    // Lane l's pieces (4 columns each) of rows l, l ^ 1, .. of its group of
+    // kN/4 lanes, from each lane's pieces of its own row, and back: so that a
+    // group of lanes reads or writes whole rows.
+    static __device__ __forceinline__ void exchange(float (&v)[kN], int lane)
+    {
+#pragma unroll
+        for (int m = 1; m < kN / 4; m *= 2)
+#pragma unroll
+            for (int i = 0; i < kN / 4; ++i) {
+                if (i & m) continue;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const bool up = lane & m;
+                    const float t = __shfl_xor_sync(0xffffffffu, up ? v[4 * i + q] : v[4 * (i | m) + q], m);
+                    if (up) v[4 * i + q] = t;
+                    else v[4 * (i | m) + q] = t;
+                }
+            }
+    }
     // the caller's states, [N,H,Dx,Dz] or transposed: once per segment
-    __device__ __forceinline__ void load(const float *src, float w)
+    __device__ __forceinline__ void load(const float *src)
     {
         src += head * p.Dx * p.Dz;
-        const int step = p.state_t ? p.Dx : 1;
-        src += p.state_t ? (size_t)dz0 * p.Dx + dx : (size_t)dx * p.Dz + dz0;
+        if (p.state_t) {
 #pragma unroll
-        for (int q = 0; q < kN; ++q) s[q] = dx < p.Dx && dz0 + q < p.Dz ? w * __ldcg(src + (size_t)q * step) : 0.f;
+            for (int q = 0; q < kN; ++q)
+                s[q] = dx < p.Dx && dz0 + q < p.Dz ? __ldcg(src + (size_t)(dz0 + q) * p.Dx + dx) : 0.f;
+            return;
+        }
+        const int c0 = dz0 + 4 * (lane % (kN / 4)), r0 = 32 * quarter + lane / (kN / 4) * (kN / 4);
+#pragma unroll
+        for (int i = 0; i < kN / 4; ++i) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r0 + i < p.Dx && c0 < p.Dz) v = __ldcg((const float4 *)(src + (size_t)(r0 + i) * p.Dz + c0));
+            s[4 * i] = v.x;
+            s[4 * i + 1] = v.y;
+            s[4 * i + 2] = v.z;
+            s[4 * i + 3] = v.w;
+        }
+        exchange(s, lane);
     }
-    __device__ __forceinline__ void store(float *dst) const
+    // the last use of the state: it is not in order afterwards
+    __device__ __forceinline__ void store(float *dst)
     {
         dst += head * p.Dx * p.Dz;
-        const int step = p.state_t ? p.Dx : 1;
-        dst += p.state_t ? (size_t)dz0 * p.Dx + dx : (size_t)dx * p.Dz + dz0;
+        if (p.state_t) {
 #pragma unroll
-        for (int q = 0; q < kN; ++q)
-            if (dx < p.Dx && dz0 + q < p.Dz) dst[(size_t)q * step] = s[q];
+            for (int q = 0; q < kN; ++q)
+                if (dx < p.Dx && dz0 + q < p.Dz) dst[(size_t)(dz0 + q) * p.Dx + dx] = s[q];
+            return;
+        }
+        exchange(s, lane);
+        const int c0 = dz0 + 4 * (lane % (kN / 4)), r0 = 32 * quarter + lane / (kN / 4) * (kN / 4);
+#pragma unroll
+        for (int i = 0; i < kN / 4; ++i)
+            if (r0 + i < p.Dx && c0 < p.Dz)
+                *(float4 *)(dst + (size_t)(r0 + i) * p.Dz + c0) =
+                    make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
     }
     // a segment's state in the workspace, in an order of the threads' own
     __device__ __forceinline__ float4 *part(int slot) const
@@ -637,7 +678,7 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
         // The sequence's own initial state runs on through its first
         // segment's state. The copy is for the kernel that starts from it: by
         // then the caller's may hold the final state already.
-        e.load(p.init, 1.f);
+        e.load(p.init);
         e.store_part(REV ? 0 : p.P - 1);
     }
 #pragma unroll 1
@@ -690,12 +731,11 @@ la_state_kernel(const __grid_constant__ CUtensorMap my, const __grid_constant__ 
     uint32_t *slot = setup<REV>(c, p, smem);
     if (misplaced(c)) return;
     if (REV ? c.g.rank > c.last_rank : c.g.rank >= c.last_rank) return;   // no segment follows it
-    if (threadIdx.x == 0) {
-#pragma unroll 1
-        for (int i = 0; i < kBars; ++i)
-            mbar_init(&c.bar[i], i >= bYReady && i < bYFree                                      ? 4
-                                 : (i >= bEmptyY && i < bEmptyZ) || (i >= bBFree && i <= bZReady) ? kStateWarps
-                                                                                                : 1);
+    if (threadIdx.x < kBars) {
+        const int i = threadIdx.x;
+        mbar_init(&c.bar[i], i >= bYReady && i < bYFree                                         ? 4
+                             : (i >= bEmptyY && i < bEmptyZ) || (i >= bBFree && i <= bZReady) ? kStateWarps
+                                                                                              : 1);
         fence_mbar_init();
     }
     const int warp = uni((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
@@ -1017,7 +1057,7 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
     // launch before this one
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (c.last_rank == 0 || c.chunks == 0) {
-        if (p.init) e.load(p.init, 1.f);
+        if (p.init) e.load(p.init);
     } else if (c.g.rank == first_rank) {
         if (p.init) e.add_part(REV ? 0 : p.P - 1, 1.f);
     } else {
@@ -1113,19 +1153,15 @@ la_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
     if (misplaced(c)) return;
     c.has0 = p.init != nullptr || (REV ? c.g.rank < c.last_rank : c.g.rank > 0);
     c.updates = c.chunks - (p.fin && c.g.rank == (REV ? 0 : c.last_rank) ? 0 : 1);
-    if (threadIdx.x == 0) {
-#pragma unroll 1
-        for (int i = 0; i < kBars; ++i) {
-            const int n = i == bOutFree || i == bStaged                                     ? kOutWarps
-                          : i == bAReady                                                    ? 2 * kOutWarps
-                          : i == bInterReady                                                ? kStateWarps
-                          : i == bYReady || i == bYReady + 1                                ? kStateWarps / 2
-                          : i == bBFree || i == bStateReady || i == bZReady                 ? kStateWarps
-                          : i == bEmptyY || i == bEmptyY + 1                                ? kStateWarps + 1
-                          : i == bEmptyZ || i == bEmptyZ + 1                                ? 2
-                                                                                            : 1;
-            mbar_init(&c.bar[i], n);
-        }
+    if (threadIdx.x < kBars) {
+        const int i = threadIdx.x;
+        mbar_init(&c.bar[i], i == bOutFree || i == bStaged                     ? kOutWarps
+                             : i == bAReady                                    ? 2 * kOutWarps
+                             : i == bYReady || i == bYReady + 1                ? kStateWarps / 2
+                             : i == bEmptyY || i == bEmptyY + 1                ? kStateWarps + 1
+                             : i == bEmptyZ || i == bEmptyZ + 1                ? 2
+                             : i == bInterReady || i == bBFree || i == bStateReady || i == bZReady ? kStateWarps
+                                                                                                   : 1);
         fence_mbar_init();
     }
     const int warp = uni((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
