@@ -682,7 +682,9 @@ dp_status make_gn(const dp_gn_dims *d, dp::GroupNorm *p)
     if (d->dtype != DP_F32 && d->dtype != DP_BF16) return DP_ERR_INVALID_ARG;
     if (d->act != DP_ACT_NONE && d->act != DP_ACT_SILU) return DP_ERR_INVALID_ARG;
     if (!(d->eps >= 0.f) || d->eps > 3.4e38f) return DP_ERR_INVALID_ARG;
-    // the grids are at most one CTA per (sample, group); rows fit an int
+    // the grids are at most one CTA per (sample, group), or per row, by one per
+    // 32 channels
+    if (d->C > (1 << 20)) return DP_ERR_UNSUPPORTED;
     if ((long long)d->N * d->G > 0x7fffffffll || (long long)d->N * d->S > 0x7fffffffll) return DP_ERR_UNSUPPORTED;
     memset(p, 0, sizeof(*p));
     p->N = d->N; p->S = d->S; p->C = d->C; p->G = d->G;

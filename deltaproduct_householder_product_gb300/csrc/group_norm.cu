@@ -1,11 +1,24 @@
 // Group norm with an activation, channels last, and its gradients, fp32
 // arithmetic. x is [N, S, C]; group g of sample n is its S rows' channels
-// [g C/G, (g+1) C/G), M = S C/G values:
+// [g W, (g+1) W), W = C/G, M = S W values:
 //   mean = sum x / M,  rstd = (sum (x - mean)^2 / M + eps)^-1/2,
 //   z = (x - mean) rstd w_c + b_c,  y = act(z).
 // Gradients, with h = (x - mean) rstd, d = dy act'(z), u = d w_c:
 //   dx = rstd (u - mean_group(u) - h mean_group(u h)),
 //   dw_c = sum_{n,s} d h,  db_c = sum_{n,s} d.
+// Everything is bound by its bytes; the forms differ in where a group's
+// values are when its sums are known:
+//  rows       S = 1, whole 16-byte pieces in a group (up to 32 x kMaxPieces):
+//             a group is one piece a lane (or a few) of a part of a warp, and
+//             stays in registers; one launch, every byte once.
+//  tiles      S = 1, groups of any other width: rows staged in shared memory,
+//             a part of a warp per group; one launch.
+//  positions  S > 1: a slice of a sample's rows per CTA, its threads on fixed
+//             channels; partial sums, then a second walk over the rows, which
+//             L2 serves where the tensor fits.
+//  wide       S = 1, what is left (very wide groups or rows): a CTA per group.
+// Squared distances are taken from the mean (or summed about a nearby value
+// and combined by counts, means and squares), never as E[x^2] - mean^2.
 #include "group_norm.h"
 
 namespace dp {
@@ -18,17 +31,77 @@ __device__ __forceinline__ float ld(const __nv_bfloat16 *p, size_t i) { return _
 __device__ __forceinline__ void st(float *p, size_t i, float x) { p[i] = x; }
 __device__ __forceinline__ void st(__nv_bfloat16 *p, size_t i, float x) { p[i] = __float2bfloat16_rn(x); }
 
-__device__ __forceinline__ float act_fwd(float z, int act)
+// K consecutive values, K = 1 or 16 bytes of them
+template <typename T, int K> struct Piece;
+template <typename T> struct Piece<T, 1> {
+    static __device__ __forceinline__ void load(const T *p, float (&f)[1]) { f[0] = ld(p, 0); }
+    static __device__ __forceinline__ void store(T *p, const float (&f)[1]) { st(p, 0, f[0]); }
+};
+template <> struct Piece<float, 4> {
+    static __device__ __forceinline__ void load(const float *p, float (&f)[4])
+    {
+        const float4 v = *(const float4 *)p;
+        f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    }
+    static __device__ __forceinline__ void store(float *p, const float (&f)[4])
+    {
+        *(float4 *)p = make_float4(f[0], f[1], f[2], f[3]);
+    }
+};
+template <> struct Piece<__nv_bfloat16, 8> {
+    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&f)[8])
+    {
+        const uint4 v = *(const uint4 *)p;
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&f)[8])
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+        *(uint4 *)p = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <typename T> struct Vec { static constexpr int n = 16 / sizeof(T); };
+
+// The sigmoid's exponential and division: exact functions for fp32 results,
+// the hardware approximations (some 2^-21) where the result is rounded to 8
+// bits. sigmoid(z) and 1 - sigmoid(z) from e^-|z|, so that neither cancels.
+template <typename T> __device__ __forceinline__ float act_fwd(float z, int act);
+template <> __device__ __forceinline__ float act_fwd<float>(float z, int act)
 {
     return act == DP_ACT_SILU ? z / (1.f + expf(-z)) : z;
 }
+template <> __device__ __forceinline__ float act_fwd<__nv_bfloat16>(float z, int act)
+{
+    return act == DP_ACT_SILU ? __fdividef(z, 1.f + __expf(-z)) : z;
+}
+template <typename T> __device__ __forceinline__ float exp_neg(float a);
+template <> __device__ __forceinline__ float exp_neg<float>(float a) { return expf(-a); }
+template <> __device__ __forceinline__ float exp_neg<__nv_bfloat16>(float a) { return __expf(-a); }
+template <typename T> __device__ __forceinline__ float recip(float a);
+template <> __device__ __forceinline__ float recip<float>(float a) { return 1.f / a; }
+template <> __device__ __forceinline__ float recip<__nv_bfloat16>(float a) { return __fdividef(1.f, a); }
 // act'(z); SiLU: p (1 + z (1 - p)) with p = sigmoid(z)
-__device__ __forceinline__ float act_grad(float z, int act)
+template <typename T> __device__ __forceinline__ float act_grad(float z, int act)
 {
     if (act != DP_ACT_SILU) return 1.f;
-    const float e = expf(-fabsf(z)), r = 1.f / (1.f + e);
-    const float p = z >= 0.f ? r : e * r, m = z >= 0.f ? e * r : r;   // sigmoid(z), 1 - sigmoid(z)
-    return p * (1.f + z * m);
+    const float e = exp_neg<T>(fabsf(z)), r = recip<T>(1.f + e);
+    const float p = z >= 0.f ? r : e * r, m = z >= 0.f ? e * r : r;
+    return p * fmaf(z, m, 1.f);
+}
+
+// sum over the `lanes` (a power of two) neighbouring lanes of a group
+__device__ __forceinline__ float lane_sum(float v, int lanes)
+{
+    for (int m = lanes >> 1; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
 }
 
 // sums over the CTA, the same in every thread
@@ -36,11 +109,8 @@ __device__ __forceinline__ float2 block_sum(float a, float b)
 {
     __shared__ float2 red[kThreads / 32];
     __syncthreads();
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, m);
-        b += __shfl_xor_sync(0xffffffffu, b, m);
-    }
+    a = lane_sum(a, 32);
+    b = lane_sum(b, 32);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
     __syncthreads();
     a = b = 0.f;
@@ -52,36 +122,374 @@ __device__ __forceinline__ float2 block_sum(float a, float b)
     return make_float2(a, b);
 }
 
+// ---------------------------------------------------------------- rows
+// A row's groups take `lanes` lanes each (the power of two that holds their
+// pieces, or 32 with V pieces a lane); a thread keeps its channels for all the
+// rows it walks, so weights stay in registers, and the gradients' channel
+// sums too. kRows rows are in flight at once.
+struct RowMap {
+    int lanes, pieces;      // of a group
+    int slots, per;         // lanes of a row; rows that a CTA takes at once (1 if the row needs several CTAs)
+};
+
+RowMap row_map(const GroupNorm &p, int vec)
+{
+    RowMap m;
+    m.pieces = p.C / p.G / vec;
+    m.lanes = 1;
+    while (m.lanes < m.pieces && m.lanes < 32) m.lanes *= 2;
+    m.slots = p.G * m.lanes;
+    m.per = m.slots < kThreads ? kThreads / m.slots : 1;
+    return m;
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads)
+gn_rows_kernel(GroupNorm p, RowMap m)
+{
+    constexpr int K = Vec<T>::n, kRows = V == 1 ? 2 : 1;
+    const int W = p.C / p.G;
+    const int slot = m.per > 1 ? threadIdx.x % m.slots : blockIdx.y * kThreads + threadIdx.x;
+    const int sub = m.per > 1 ? threadIdx.x / m.slots : 0;
+    const bool in = sub < m.per && slot < m.slots;
+    const int g = in ? slot / m.lanes : 0, l = slot & (m.lanes - 1);
+    const float inv = 1.f / (float)W;
+    float w[V][K], b[V][K];
+    bool on[V];
+    size_t at[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        on[v] = in && l + v * m.lanes < m.pieces;
+        at[v] = (size_t)g * W + (size_t)(l + v * m.lanes) * K;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            w[v][k] = 1.f;
+            b[v][k] = 0.f;
+        }
+        if (on[v] && p.weight) Piece<T, K>::load((const T *)p.weight + at[v], w[v]);
+        if (on[v] && p.bias) Piece<T, K>::load((const T *)p.bias + at[v], b[v]);
+    }
+    const long long step = (long long)gridDim.x * m.per;
+    // every thread of a warp makes the same number of turns (the lanes' sums)
+    for (long long n0 = (long long)blockIdx.x * m.per; n0 < p.N; n0 += step * kRows) {
+        float x[kRows][V][K];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) x[r][v][k] = 0.f;
+                const long long n = n0 + r * step + sub;
+                if (on[v] && n < p.N) Piece<T, K>::load((const T *)p.x + (size_t)n * p.C + at[v], x[r][v]);
+            }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const long long n = n0 + r * step + sub;
+            float sum = 0.f, sq = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int k = 0; k < K; ++k) sum += x[r][v][k];
+            const float mean = lane_sum(sum, m.lanes) * inv;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (on[v])
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        x[r][v][k] -= mean;
+                        sq = fmaf(x[r][v][k], x[r][v][k], sq);
+                    }
+            const float rstd = 1.f / sqrtf(fmaf(lane_sum(sq, m.lanes), inv, p.eps));
+            if (n >= p.N) continue;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (on[v]) {
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+                        x[r][v][k] = act_fwd<T>(fmaf(x[r][v][k] * rstd, w[v][k], b[v][k]), p.act);
+                    Piece<T, K>::store((T *)p.y + (size_t)n * p.C + at[v], x[r][v]);
+                }
+            if (in && l == 0) {
+                if (p.mean) p.mean[n * p.G + g] = mean;
+                if (p.rstd) p.rstd[n * p.G + g] = rstd;
+            }
+        }
+    }
+}
+
+// Channel sums of the gradients leave each CTA as one row of partial sums
+// [slice][2][C]; gn_channel_sum_kernel adds the rows in order.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads)
+gn_rows_backward_kernel(GroupNorm p, RowMap m, float *part)
+{
+    constexpr int K = Vec<T>::n;
+    __shared__ float red[kThreads * (K + 1)];
+    const int W = p.C / p.G;
+    const int slot = m.per > 1 ? threadIdx.x % m.slots : blockIdx.y * kThreads + threadIdx.x;
+    const int sub = m.per > 1 ? threadIdx.x / m.slots : 0;
+    const bool in = sub < m.per && slot < m.slots;
+    const int g = in ? slot / m.lanes : 0, l = slot & (m.lanes - 1);
+    const float inv = 1.f / (float)W;
+    float w[V][K], b[V][K], dw[V][K], db[V][K];
+    bool on[V];
+    size_t at[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        on[v] = in && l + v * m.lanes < m.pieces;
+        at[v] = (size_t)g * W + (size_t)(l + v * m.lanes) * K;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            w[v][k] = 1.f;
+            b[v][k] = dw[v][k] = db[v][k] = 0.f;
+        }
+        if (on[v] && p.weight) Piece<T, K>::load((const T *)p.weight + at[v], w[v]);
+        if (on[v] && p.bias) Piece<T, K>::load((const T *)p.bias + at[v], b[v]);
+    }
+    const long long step = (long long)gridDim.x * m.per;
+    for (long long n0 = (long long)blockIdx.x * m.per; n0 < p.N; n0 += step) {
+        const long long n = n0 + sub;
+        const bool row = n < p.N;
+        float h[V][K], u[V][K], mean = 0.f, rstd = 0.f;
+        if (in && row) {
+            mean = p.mean[n * p.G + g];
+            rstd = p.rstd[n * p.G + g];
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) h[v][k] = u[v][k] = 0.f;
+            if (on[v] && row) {
+                Piece<T, K>::load((const T *)p.x + (size_t)n * p.C + at[v], h[v]);
+                Piece<T, K>::load((const T *)p.dy + (size_t)n * p.C + at[v], u[v]);
+            }
+        }
+        float su = 0.f, suh = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (on[v] && row)
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const float hh = (h[v][k] - mean) * rstd;
+                    const float d = u[v][k] * act_grad<T>(fmaf(hh, w[v][k], b[v][k]), p.act);
+                    dw[v][k] = fmaf(d, hh, dw[v][k]);
+                    db[v][k] += d;
+                    h[v][k] = hh;
+                    u[v][k] = d * w[v][k];
+                    su += u[v][k];
+                    suh = fmaf(u[v][k], hh, suh);
+                }
+        const float mu = lane_sum(su, m.lanes) * inv, muh = lane_sum(suh, m.lanes) * inv;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (on[v] && row) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) u[v][k] = rstd * (u[v][k] - mu - h[v][k] * muh);
+                Piece<T, K>::store((T *)p.dx + (size_t)n * p.C + at[v], u[v]);
+            }
+    }
+    if (!part) return;
+    // the rows that the CTA took at once share channels
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < K; ++k) red[threadIdx.x * (K + 1) + k] = which ? db[v][k] : dw[v][k];
+            __syncthreads();
+            if (sub == 0 && on[v]) {
+                float *dst = part + ((size_t)blockIdx.x * 2 + which) * p.C + at[v];
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    float s = 0.f;
+                    for (int r = 0; r < m.per; ++r) s += red[(threadIdx.x + r * m.slots) * (K + 1) + k];
+                    dst[k] = s;
+                }
+            }
+        }
+}
+
+// one warp per channel sum: lanes over the slices, then across the lanes in a
+// fixed tree
+__global__ void __launch_bounds__(kThreads)
+gn_channel_sum_kernel(GroupNorm p, int slices, const float *part)
+{
+    __shared__ float red[kThreads / 32][33];
+    // a CTA adds 32 neighbouring entries of [2][C]; warp = every 8th slice
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long i = (long long)blockIdx.x * 32 + lane;
+    float s = 0.f;
+    if (i < 2ll * p.C)
+        for (int k = warp; k < slices; k += kThreads / 32) s += part[(size_t)k * 2 * p.C + i];
+    red[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && i < 2ll * p.C) {
+        s = 0.f;
+#pragma unroll
+        for (int k = 0; k < kThreads / 32; ++k) s += red[k][lane];
+        float *dst = i < p.C ? p.dweight : p.dbias;
+        if (dst) dst[i < p.C ? i : i - p.C] = s;
+    }
+}
+
+// ---------------------------------------------------------------- tiles
+// R whole rows (R C a multiple of 16 bytes' values where there are that many
+// rows) through shared memory as fp32; `lanes` lanes walk a group's W values.
+constexpr int kTileValues = 8192;
+
+struct TileMap {
+    int rows, lanes;
+};
+
+template <typename T>
+TileMap tile_map(const GroupNorm &p)
+{
+    const int unit = Vec<T>::n, W = p.C / p.G;
+    TileMap m;
+    m.rows = kTileValues / p.C / unit * unit;
+    if (m.rows < 1) m.rows = kTileValues / p.C;
+    m.lanes = 1;
+    while (m.lanes < 32 && m.lanes * 4 < W) m.lanes *= 2;
+    return m;
+}
+
+// `count` values from `at` on into shared memory, or back
+template <typename T>
+__device__ __forceinline__ void tile_in(float *dst, const T *src, size_t at, int count)
+{
+    constexpr int K = Vec<T>::n;
+    const int whole = at % K == 0 ? count / K : 0;
+    for (int i = threadIdx.x; i < whole; i += kThreads) {
+        float f[K];
+        Piece<T, K>::load(src + at + (size_t)i * K, f);
+#pragma unroll
+        for (int k = 0; k < K; ++k) dst[i * K + k] = f[k];
+    }
+    for (int i = whole * K + threadIdx.x; i < count; i += kThreads) dst[i] = ld(src, at + i);
+}
+template <typename T>
+__device__ __forceinline__ void tile_out(T *dst, const float *src, size_t at, int count)
+{
+    constexpr int K = Vec<T>::n;
+    const int whole = at % K == 0 ? count / K : 0;
+    for (int i = threadIdx.x; i < whole; i += kThreads) {
+        float f[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) f[k] = src[i * K + k];
+        Piece<T, K>::store(dst + at + (size_t)i * K, f);
+    }
+    for (int i = whole * K + threadIdx.x; i < count; i += kThreads) st(dst, at + i, src[i]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+gn_tiles_kernel(GroupNorm p, TileMap m)
+{
+    extern __shared__ float tile[];
+    const int W = p.C / p.G, l = threadIdx.x % m.lanes, groups = kThreads / m.lanes;
+    for (long long n0 = (long long)blockIdx.x * m.rows; n0 < p.N; n0 += (long long)gridDim.x * m.rows) {
+        const int rows = p.N - n0 < m.rows ? (int)(p.N - n0) : m.rows;
+        __syncthreads();
+        tile_in<T>(tile, (const T *)p.x, (size_t)n0 * p.C, rows * p.C);
+        __syncthreads();
+        for (int q0 = 0; q0 < rows * p.G; q0 += groups) {
+            const int q = q0 + threadIdx.x / m.lanes;        // row and group in one
+            const bool in = q < rows * p.G;
+            float *x = tile + (size_t)q * W;
+            float sum = 0.f, sq = 0.f;
+            if (in)
+                for (int i = l; i < W; i += m.lanes) sum += x[i];
+            const float mean = lane_sum(sum, m.lanes) / (float)W;
+            if (in)
+                for (int i = l; i < W; i += m.lanes) sq = fmaf(x[i] - mean, x[i] - mean, sq);
+            const float rstd = 1.f / sqrtf(lane_sum(sq, m.lanes) / (float)W + p.eps);
+            if (!in) continue;
+            const int c0 = q % p.G * W;
+            for (int i = l; i < W; i += m.lanes) {
+                float z = (x[i] - mean) * rstd;
+                if (p.weight) z *= ld((const T *)p.weight, c0 + i);
+                if (p.bias) z += ld((const T *)p.bias, c0 + i);
+                x[i] = act_fwd<T>(z, p.act);
+            }
+            if (l == 0) {
+                if (p.mean) p.mean[n0 * p.G + q] = mean;
+                if (p.rstd) p.rstd[n0 * p.G + q] = rstd;
+            }
+        }
+        __syncthreads();
+        tile_out<T>((T *)p.y, tile, (size_t)n0 * p.C, rows * p.C);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+gn_tiles_backward_kernel(GroupNorm p, TileMap m)
+{
+    extern __shared__ float tile[];
+    float *tx = tile, *td = tile + kTileValues;
+    const int W = p.C / p.G, l = threadIdx.x % m.lanes, groups = kThreads / m.lanes;
+    for (long long n0 = (long long)blockIdx.x * m.rows; n0 < p.N; n0 += (long long)gridDim.x * m.rows) {
+        const int rows = p.N - n0 < m.rows ? (int)(p.N - n0) : m.rows;
+        __syncthreads();
+        tile_in<T>(tx, (const T *)p.x, (size_t)n0 * p.C, rows * p.C);
+        tile_in<T>(td, (const T *)p.dy, (size_t)n0 * p.C, rows * p.C);
+        __syncthreads();
+        for (int q0 = 0; q0 < rows * p.G; q0 += groups) {
+            const int q = q0 + threadIdx.x / m.lanes;
+            const bool in = q < rows * p.G;
+            float *x = tx + (size_t)q * W, *d = td + (size_t)q * W;
+            const float mean = in ? p.mean[n0 * p.G + q] : 0.f, rstd = in ? p.rstd[n0 * p.G + q] : 0.f;
+            const int c0 = in ? q % p.G * W : 0;
+            float su = 0.f, suh = 0.f;
+            if (in)
+                for (int i = l; i < W; i += m.lanes) {
+                    const float h = (x[i] - mean) * rstd, w = p.weight ? ld((const T *)p.weight, c0 + i) : 1.f;
+                    const float z = fmaf(h, w, p.bias ? ld((const T *)p.bias, c0 + i) : 0.f);
+                    const float u = d[i] * act_grad<T>(z, p.act) * w;
+                    x[i] = h;
+                    d[i] = u;
+                    su += u;
+                    suh = fmaf(u, h, suh);
+                }
+            const float mu = lane_sum(su, m.lanes) / (float)W, muh = lane_sum(suh, m.lanes) / (float)W;
+            if (in)
+                for (int i = l; i < W; i += m.lanes) d[i] = rstd * (d[i] - mu - x[i] * muh);
+        }
+        __syncthreads();
+        tile_out<T>((T *)p.dx, td, (size_t)n0 * p.C, rows * p.C);
+    }
+}
+
+// ---------------------------------------------------------------- wide
 // One CTA per (sample, group): the mean, the squared distances from it, the
 // outputs, each in a walk over the group's values.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-gn_forward_kernel(GroupNorm p)
+gn_wide_kernel(GroupNorm p)
 {
     const T *x = (const T *)p.x, *w = (const T *)p.weight, *b = (const T *)p.bias;
     T *y = (T *)p.y;
-    const int W = p.C / p.G, g = blockIdx.x % p.G, n = blockIdx.x / p.G;
-    const size_t base = (size_t)n * p.S * p.C + (size_t)g * W, m = (size_t)p.S * W;
-    const auto at = [&](size_t i) { return base + (i / W) * p.C + i % W; };
+    const int W = p.C / p.G, g = blockIdx.x % p.G;
+    const size_t base = (size_t)blockIdx.x * W;     // S = 1: groups are contiguous
     float sum = 0.f;
-    for (size_t i = threadIdx.x; i < m; i += kThreads) sum += ld(x, at(i));
-    const float mean = block_sum(sum, 0.f).x / (float)m;
+    for (int i = threadIdx.x; i < W; i += kThreads) sum += ld(x, base + i);
+    const float mean = block_sum(sum, 0.f).x / (float)W;
     float sq = 0.f;
-    for (size_t i = threadIdx.x; i < m; i += kThreads) {
-        const float d = ld(x, at(i)) - mean;
+    for (int i = threadIdx.x; i < W; i += kThreads) {
+        const float d = ld(x, base + i) - mean;
         sq = fmaf(d, d, sq);
     }
-    const float rstd = 1.f / sqrtf(block_sum(sq, 0.f).x / (float)m + p.eps);
+    const float rstd = 1.f / sqrtf(block_sum(sq, 0.f).x / (float)W + p.eps);
     if (threadIdx.x == 0) {
         if (p.mean) p.mean[blockIdx.x] = mean;
         if (p.rstd) p.rstd[blockIdx.x] = rstd;
     }
-    for (size_t i = threadIdx.x; i < m; i += kThreads) {
-        const int c = g * W + (int)(i % W);
-        float z = (ld(x, at(i)) - mean) * rstd;
-        if (w) z *= ld(w, c);
-        if (b) z += ld(b, c);
-        st(y, at(i), act_fwd(z, p.act));
+    for (int i = threadIdx.x; i < W; i += kThreads) {
+        float z = (ld(x, base + i) - mean) * rstd;
+        if (w) z *= ld(w, (size_t)g * W + i);
+        if (b) z += ld(b, (size_t)g * W + i);
+        st(y, base + i, act_fwd<T>(z, p.act));
     }
 }
 
@@ -92,52 +500,52 @@ __device__ __forceinline__ float2 grad_of(const GroupNorm &p, size_t i, int c, f
     float z = h;
     if (p.weight) z *= ld((const T *)p.weight, c);
     if (p.bias) z += ld((const T *)p.bias, c);
-    return make_float2(ld((const T *)p.dy, i) * act_grad(z, p.act), h);
+    return make_float2(ld((const T *)p.dy, i) * act_grad<T>(z, p.act), h);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-gn_backward_kernel(GroupNorm p)
+gn_wide_backward_kernel(GroupNorm p)
 {
-    const int W = p.C / p.G, g = blockIdx.x % p.G, n = blockIdx.x / p.G;
-    const size_t base = (size_t)n * p.S * p.C + (size_t)g * W, m = (size_t)p.S * W;
+    const int W = p.C / p.G, g = blockIdx.x % p.G;
+    const size_t base = (size_t)blockIdx.x * W;
     const float mean = p.mean[blockIdx.x], rstd = p.rstd[blockIdx.x];
-    const auto at = [&](size_t i) { return base + (i / W) * p.C + i % W; };
-    const auto u_of = [&](size_t i, float &h) {
-        const int c = g * W + (int)(i % W);
-        const float2 dh = grad_of<T>(p, at(i), c, mean, rstd);
+    const auto u_of = [&](int i, float &h) {
+        const int c = g * W + i;
+        const float2 dh = grad_of<T>(p, base + i, c, mean, rstd);
         h = dh.y;
         return p.weight ? dh.x * ld((const T *)p.weight, c) : dh.x;
     };
     float su = 0.f, suh = 0.f, h;
-    for (size_t i = threadIdx.x; i < m; i += kThreads) {
+    for (int i = threadIdx.x; i < W; i += kThreads) {
         const float u = u_of(i, h);
         su += u;
         suh = fmaf(u, h, suh);
     }
     const float2 s = block_sum(su, suh);
-    const float mu = s.x / (float)m, muh = s.y / (float)m;
-    for (size_t i = threadIdx.x; i < m; i += kThreads) {
+    const float mu = s.x / (float)W, muh = s.y / (float)W;
+    // every value is read before dx, which may lie over dy, is written to it
+    for (int i = threadIdx.x; i < W; i += kThreads) {
         const float u = u_of(i, h);
-        st((T *)p.dx, at(i), rstd * (u - mu - h * muh));
+        st((T *)p.dx, base + i, rstd * (u - mu - h * muh));
     }
 }
 
-// Channel sums in two steps without atomics: CTA (slice, 32 channels) adds
-// its rows, then one thread per channel adds the slices in order.
+// Channel sums for the tile and wide forms: a CTA adds the rows of its slice
+// for 32 channels. (dx is written after, where it may lie over dy.)
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 gn_channel_partial_kernel(GroupNorm p, int slices, float *part)
 {
     __shared__ float red[2][kThreads / 32][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.y * 32 + lane;
-    const long long rows = (long long)p.N * p.S, per = (rows + slices - 1) / slices;
-    const long long r0 = blockIdx.x * per, r1 = r0 + per < rows ? r0 + per : rows;
+    const long long per = (p.N + slices - 1) / slices;
+    const long long r0 = blockIdx.x * per, r1 = r0 + per < p.N ? r0 + per : p.N;
     float dw = 0.f, db = 0.f;
     if (c < p.C) {
         const int g = c / (p.C / p.G);
         for (long long r = r0 + warp; r < r1; r += kThreads / 32) {
-            const size_t ng = (size_t)(r / p.S) * p.G + g;
+            const size_t ng = (size_t)r * p.G + g;
             const float2 dh = grad_of<T>(p, (size_t)r * p.C + c, c, p.mean[ng], p.rstd[ng]);
             dw = fmaf(dh.x, dh.y, dw);
             db += dh.x;
@@ -154,47 +562,447 @@ gn_channel_partial_kernel(GroupNorm p, int slices, float *part)
     }
 }
 
-__global__ void gn_channel_sum_kernel(GroupNorm p, int slices, const float *part)
+// ---------------------------------------------------------------- positions
+// CTA (sample and slice of its rows, block of channels): `cols` threads on
+// K channels each, `rows` of them side by side.
+struct PositionMap {
+    int K, cols, rows;      // channels of a thread; threads along the channels, along the rows
+    int blocks;             // blocks of cols K channels
+    int slices, per;        // slices of a sample; rows of a slice
+};
+
+PositionMap position_map(const GroupNorm &p, int vec)
 {
-    const int i = blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= 2 * p.C) return;
-    const int which = i / p.C, c = i - which * p.C;
-    float s = 0.f;
-    for (int k = 0; k < slices; ++k) s += part[((size_t)k * 2 + which) * p.C + c];
-    float *dst = which ? p.dbias : p.dweight;
-    if (dst) dst[c] = s;
+    PositionMap m;
+    m.K = p.C % vec == 0 ? vec : 1;
+    const int pieces = p.C / m.K;
+    m.cols = pieces < kThreads ? pieces : kThreads;
+    m.rows = kThreads / m.cols;
+    m.blocks = (pieces + m.cols - 1) / m.cols;
+    // about two CTAs for each of the SMs, and at least four turns for each
+    const long long want = (2 * 152 + p.N * m.blocks - 1) / (p.N * m.blocks);
+    const long long most = (p.S + 4 * m.rows - 1) / (4 * m.rows);
+    m.slices = (int)(want < most ? want : most);
+    if (m.slices < 1) m.slices = 1;
+    m.per = (p.S + m.slices - 1) / m.slices;
+    m.slices = (p.S + m.per - 1) / m.per;
+    return m;
+}
+
+// The channel's sums about its first value in the slice, as a count, a mean
+// and the squares about it; partial results [n][slice][2][C]: mean, squares.
+template <typename T, int K>
+__global__ void __launch_bounds__(kThreads)
+gn_position_stats_kernel(GroupNorm p, PositionMap m, float *part)
+{
+    __shared__ float red[2][kThreads * K];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int col = threadIdx.x % m.cols, row = threadIdx.x / m.cols;
+    const int piece = blockIdx.y * m.cols + col;
+    const long long n = blockIdx.x / m.slices;
+    const int slice = (int)(blockIdx.x - n * m.slices);
+    const bool in = row < m.rows && piece * K < p.C;
+    const int s0 = slice * m.per, s1 = s0 + m.per < p.S ? s0 + m.per : p.S;
+    const T *x = (const T *)p.x + (size_t)n * p.S * p.C + (size_t)piece * K;
+    float base[K], a[K], q[K];
+    if (in) {
+        Piece<T, K>::load(x + (size_t)s0 * p.C, base);
+#pragma unroll
+        for (int k = 0; k < K; ++k) a[k] = q[k] = 0.f;
+        int s = s0 + row;
+        for (; s + 3 * m.rows < s1; s += 4 * m.rows) {
+            float f[4][K];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) Piece<T, K>::load(x + (size_t)(s + i * m.rows) * p.C, f[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const float d = f[i][k] - base[k];
+                    a[k] += d;
+                    q[k] = fmaf(d, d, q[k]);
+                }
+        }
+        for (; s < s1; s += m.rows) {
+            float f[K];
+            Piece<T, K>::load(x + (size_t)s * p.C, f);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const float d = f[k] - base[k];
+                a[k] += d;
+                q[k] = fmaf(d, d, q[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            red[0][(row * m.cols + col) * K + k] = a[k];
+            red[1][(row * m.cols + col) * K + k] = q[k];
+        }
+    }
+    __syncthreads();
+    if (!in || row != 0) return;
+    float *dst = part + ((size_t)n * m.slices + slice) * 2 * p.C + (size_t)piece * K;
+    const float inv = 1.f / (float)(s1 - s0);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        float sa = 0.f, sq = 0.f;
+        for (int r = 0; r < m.rows; ++r) {
+            sa += red[0][(r * m.cols + col) * K + k];
+            sq += red[1][(r * m.cols + col) * K + k];
+        }
+        dst[k] = fmaf(sa, inv, base[k]);
+        dst[p.C + k] = fmaxf(sq - sa * (sa * inv), 0.f);
+    }
+}
+
+// (n, g): the mean of the channels' means by counts, the squares about it
+__global__ void __launch_bounds__(kThreads)
+gn_position_combine_kernel(GroupNorm p, PositionMap m, const float *part, float *mean_out, float *rstd_out)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int W = p.C / p.G, g = blockIdx.x % p.G;
+    const long long n = blockIdx.x / p.G;
+    const float *src = part + (size_t)n * m.slices * 2 * p.C + (size_t)g * W;
+    const int last = p.S - (m.slices - 1) * m.per;
+    // about the first channel's mean, so that the sums hold differences only
+    const float base = src[0];
+    float sum = 0.f, sq = 0.f;
+    for (int i = threadIdx.x; i < m.slices * W; i += kThreads) {
+        const int k = i / W, c = i - k * W;
+        const float cnt = (float)(k == m.slices - 1 ? last : m.per);
+        const float d = src[(size_t)k * 2 * p.C + c] - base;
+        sum = fmaf(cnt, d, sum);
+        sq += fmaf(cnt * d, d, src[(size_t)k * 2 * p.C + p.C + c]);
+    }
+    const float2 s = block_sum(sum, sq);
+    const float inv = 1.f / ((float)p.S * (float)W), d = s.x * inv;
+    if (threadIdx.x == 0) {
+        mean_out[blockIdx.x] = base + d;
+        rstd_out[blockIdx.x] = 1.f / sqrtf(fmaxf(s.y * inv - d * d, 0.f) + p.eps);
+    }
+}
+
+// what a thread holds of its channels
+template <typename T, int K> struct Channels {
+    float w[K], b[K], mean[K], rstd[K];
+    __device__ __forceinline__ void load(const GroupNorm &p, const float *mean_, const float *rstd_, long long n, int c)
+    {
+        const int W = p.C / p.G;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const size_t ng = (size_t)n * p.G + (c + k) / W;
+            w[k] = p.weight ? ld((const T *)p.weight, c + k) : 1.f;
+            b[k] = p.bias ? ld((const T *)p.bias, c + k) : 0.f;
+            mean[k] = mean_[ng];
+            rstd[k] = rstd_[ng];
+        }
+    }
+};
+
+template <typename T, int K>
+__global__ void __launch_bounds__(kThreads)
+gn_position_apply_kernel(GroupNorm p, PositionMap m, const float *mean, const float *rstd)
+{
+    const int col = threadIdx.x % m.cols, row = threadIdx.x / m.cols;
+    const int piece = blockIdx.y * m.cols + col;
+    const long long n = blockIdx.x / m.slices;
+    const int slice = (int)(blockIdx.x - n * m.slices);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (row >= m.rows || piece * K >= p.C) return;
+    Channels<T, K> ch;
+    ch.load(p, mean, rstd, n, piece * K);
+    const int s0 = slice * m.per, s1 = s0 + m.per < p.S ? s0 + m.per : p.S;
+    const size_t at = (size_t)n * p.S * p.C + (size_t)piece * K;
+#pragma unroll 4
+    for (int s = s0 + row; s < s1; s += m.rows) {
+        float f[K];
+        Piece<T, K>::load((const T *)p.x + at + (size_t)s * p.C, f);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            f[k] = act_fwd<T>(fmaf((f[k] - ch.mean[k]) * ch.rstd[k], ch.w[k], ch.b[k]), p.act);
+        Piece<T, K>::store((T *)p.y + at + (size_t)s * p.C, f);
+    }
+}
+
+// per channel of a slice: sums of d h and of d, which are both the gradients'
+// channel sums and, weighted, the groups' sums of u h and u
+template <typename T, int K>
+__global__ void __launch_bounds__(kThreads)
+gn_position_grad_kernel(GroupNorm p, PositionMap m, float *part)
+{
+    __shared__ float red[2][kThreads * K];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int col = threadIdx.x % m.cols, row = threadIdx.x / m.cols;
+    const int piece = blockIdx.y * m.cols + col;
+    const long long n = blockIdx.x / m.slices;
+    const int slice = (int)(blockIdx.x - n * m.slices);
+    const bool in = row < m.rows && piece * K < p.C;
+    if (in) {
+        Channels<T, K> ch;
+        ch.load(p, p.mean, p.rstd, n, piece * K);
+        const int s0 = slice * m.per, s1 = s0 + m.per < p.S ? s0 + m.per : p.S;
+        const size_t at = (size_t)n * p.S * p.C + (size_t)piece * K;
+        float a[K], q[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) a[k] = q[k] = 0.f;
+#pragma unroll 2
+        for (int s = s0 + row; s < s1; s += m.rows) {
+            float x[K], d[K];
+            Piece<T, K>::load((const T *)p.x + at + (size_t)s * p.C, x);
+            Piece<T, K>::load((const T *)p.dy + at + (size_t)s * p.C, d);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const float h = (x[k] - ch.mean[k]) * ch.rstd[k];
+                const float dd = d[k] * act_grad<T>(fmaf(h, ch.w[k], ch.b[k]), p.act);
+                a[k] = fmaf(dd, h, a[k]);
+                q[k] += dd;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            red[0][(row * m.cols + col) * K + k] = a[k];
+            red[1][(row * m.cols + col) * K + k] = q[k];
+        }
+    }
+    __syncthreads();
+    if (!in || row != 0) return;
+    float *dst = part + ((size_t)n * m.slices + slice) * 2 * p.C + (size_t)piece * K;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        for (int which = 0; which < 2; ++which) {
+            float s = 0.f;
+            for (int r = 0; r < m.rows; ++r) s += red[which][(r * m.cols + col) * K + k];
+            dst[which * p.C + k] = s;
+        }
+}
+
+// (n, g): E[u h] and E[u]
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+gn_position_grad_combine_kernel(GroupNorm p, PositionMap m, const float *part, float2 *sums)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int W = p.C / p.G, g = blockIdx.x % p.G;
+    const long long n = blockIdx.x / p.G;
+    const float *src = part + (size_t)n * m.slices * 2 * p.C + (size_t)g * W;
+    float a = 0.f, b = 0.f;
+    for (int i = threadIdx.x; i < m.slices * W; i += kThreads) {
+        const int k = i / W, c = i - k * W;
+        const float w = p.weight ? ld((const T *)p.weight, (size_t)g * W + c) : 1.f;
+        a = fmaf(w, src[(size_t)k * 2 * p.C + c], a);
+        b = fmaf(w, src[(size_t)k * 2 * p.C + p.C + c], b);
+    }
+    const float2 s = block_sum(a, b);
+    const float inv = 1.f / ((float)p.S * (float)W);
+    if (threadIdx.x == 0) sums[blockIdx.x] = make_float2(s.x * inv, s.y * inv);
+}
+
+template <typename T, int K>
+__global__ void __launch_bounds__(kThreads)
+gn_position_dx_kernel(GroupNorm p, PositionMap m, const float2 *sums)
+{
+    const int col = threadIdx.x % m.cols, row = threadIdx.x / m.cols;
+    const int piece = blockIdx.y * m.cols + col;
+    const long long n = blockIdx.x / m.slices;
+    const int slice = (int)(blockIdx.x - n * m.slices);
+    const bool in = row < m.rows && piece * K < p.C;
+    Channels<T, K> ch;
+    if (in) ch.load(p, p.mean, p.rstd, n, piece * K);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!in) return;
+    float muh[K], mu[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const float2 s = sums[(size_t)n * p.G + (piece * K + k) / (p.C / p.G)];
+        muh[k] = s.x;
+        mu[k] = s.y;
+    }
+    const int s0 = slice * m.per, s1 = s0 + m.per < p.S ? s0 + m.per : p.S;
+    const size_t at = (size_t)n * p.S * p.C + (size_t)piece * K;
+#pragma unroll 2
+    for (int s = s0 + row; s < s1; s += m.rows) {
+        float x[K], d[K];
+        Piece<T, K>::load((const T *)p.x + at + (size_t)s * p.C, x);
+        Piece<T, K>::load((const T *)p.dy + at + (size_t)s * p.C, d);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float h = (x[k] - ch.mean[k]) * ch.rstd[k];
+            const float u = d[k] * act_grad<T>(fmaf(h, ch.w[k], ch.b[k]), p.act) * ch.w[k];
+            d[k] = ch.rstd[k] * (u - mu[k] - h * muh[k]);
+        }
+        Piece<T, K>::store((T *)p.dx + at + (size_t)s * p.C, d);
+    }
+}
+
+// ---------------------------------------------------------------- which form
+enum Form { kFormRows, kFormTiles, kFormPositions, kFormWide };
+constexpr int kMaxPieces = 4;        // of a lane, forward
+constexpr int kMaxPiecesGrad = 2;    // with gradients (registers)
+
+Form form_of(const GroupNorm &p, bool grad)
+{
+    const int vec = p.dtype == DP_F32 ? 4 : 8, W = p.C / p.G;
+    if (p.S > 1) return kFormPositions;
+    if (W % vec == 0 && W / vec <= 32 * (grad ? kMaxPiecesGrad : kMaxPieces)) return kFormRows;
+    return p.C <= kTileValues ? kFormTiles : kFormWide;
+}
+
+int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+
+// row-form CTAs along the rows: enough to fill the SMs several times over,
+// each with rows to walk
+int row_ctas(const GroupNorm &p, const RowMap &m, int per_sm)
+{
+    const long long most = ceil_div(p.N, m.per), cols = ceil_div(m.slots, kThreads);
+    const long long want = 152ll * per_sm / (m.per > 1 ? 1 : cols);
+    return (int)(want < 1 ? 1 : want < most ? want : most);
 }
 
 int channel_slices(const GroupNorm &p)
 {
-    const long long rows = (long long)p.N * p.S;
-    return (int)(rows < 64 ? 1 : rows / 64 < 256 ? rows / 64 : 256);
+    return (int)(p.N < 64 ? 1 : p.N / 64 < 256 ? p.N / 64 : 256);
+}
+
+size_t position_part_values(const GroupNorm &p, const PositionMap &m) { return (size_t)p.N * m.slices * 2 * p.C; }
+
+template <typename... A, typename... B>
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, cudaStream_t stream, B... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename T, int K>
+cudaError_t forward_positions(const GroupNorm &p, const PositionMap &m)
+{
+    const dim3 grid((unsigned)(p.N * m.slices), m.blocks);
+    float *part = p.scratch, *mean = p.mean, *rstd = p.rstd;
+    if (!mean) mean = part + position_part_values(p, m);
+    if (!rstd) rstd = part + position_part_values(p, m) + (size_t)p.N * p.G;
+    gn_position_stats_kernel<T, K><<<grid, kThreads, 0, p.stream>>>(p, m, part);
+    cudaError_t e = launch_after(gn_position_combine_kernel, dim3((unsigned)(p.N * p.G)), p.stream, p, m,
+                                 (const float *)part, mean, rstd);
+    if (e != cudaSuccess) return e;
+    return launch_after(gn_position_apply_kernel<T, K>, grid, p.stream, p, m, (const float *)mean, (const float *)rstd);
+}
+
+template <typename T, int K>
+cudaError_t backward_positions(const GroupNorm &p, const PositionMap &m)
+{
+    const dim3 grid((unsigned)(p.N * m.slices), m.blocks);
+    float *part = p.scratch;
+    float2 *sums = (float2 *)(part + position_part_values(p, m));
+    gn_position_grad_kernel<T, K><<<grid, kThreads, 0, p.stream>>>(p, m, part);
+    cudaError_t e = launch_after(gn_position_grad_combine_kernel<T>, dim3((unsigned)(p.N * p.G)), p.stream, p, m,
+                                 (const float *)part, sums);
+    if (e != cudaSuccess) return e;
+    e = launch_after(gn_position_dx_kernel<T, K>, grid, p.stream, p, m, (const float2 *)sums);
+    if (e != cudaSuccess || !(p.dweight || p.dbias)) return e;
+    gn_channel_sum_kernel<<<ceil_div(2ll * p.C, 32), kThreads, 0, p.stream>>>(p, (int)(p.N * m.slices), part);
+    return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t forward_typed(const GroupNorm &p)
 {
-    gn_forward_kernel<T><<<(unsigned)(p.N * p.G), kThreads, 0, p.stream>>>(p);
+    constexpr int K = Vec<T>::n;
+    switch (form_of(p, false)) {
+    case kFormRows: {
+        const RowMap m = row_map(p, K);
+        const dim3 grid(row_ctas(p, m, 8), m.per > 1 ? 1 : ceil_div(m.slots, kThreads));
+        const int v = ceil_div(m.pieces, m.lanes);
+        if (v == 1) gn_rows_kernel<T, 1><<<grid, kThreads, 0, p.stream>>>(p, m);
+        else if (v == 2) gn_rows_kernel<T, 2><<<grid, kThreads, 0, p.stream>>>(p, m);
+        else gn_rows_kernel<T, 4><<<grid, kThreads, 0, p.stream>>>(p, m);
+        break;
+    }
+    case kFormTiles: {
+        const TileMap m = tile_map<T>(p);
+        const int most = ceil_div(p.N, m.rows);
+        gn_tiles_kernel<T><<<most < 152 * 6 ? most : 152 * 6, kThreads, kTileValues * sizeof(float), p.stream>>>(p, m);
+        break;
+    }
+    case kFormPositions: {
+        const PositionMap m = position_map(p, K);
+        return m.K == K ? forward_positions<T, K>(p, m) : forward_positions<T, 1>(p, m);
+    }
+    default: gn_wide_kernel<T><<<(unsigned)(p.N * p.G), kThreads, 0, p.stream>>>(p);
+    }
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t backward_typed(const GroupNorm &p)
 {
-    gn_backward_kernel<T><<<(unsigned)(p.N * p.G), kThreads, 0, p.stream>>>(p);
-    if (p.dweight || p.dbias) {
-        const int k = channel_slices(p);
-        gn_channel_partial_kernel<T><<<dim3(k, (p.C + 31) / 32), kThreads, 0, p.stream>>>(p, k, p.scratch);
-        gn_channel_sum_kernel<<<(2 * p.C + 255) / 256, 256, 0, p.stream>>>(p, k, p.scratch);
+    constexpr int K = Vec<T>::n;
+    const bool sums = p.dweight || p.dbias;
+    switch (form_of(p, true)) {
+    case kFormRows: {
+        const RowMap m = row_map(p, K);
+        const int ctas = row_ctas(p, m, 4);
+        const dim3 grid(ctas, m.per > 1 ? 1 : ceil_div(m.slots, kThreads));
+        float *part = sums ? p.scratch : nullptr;
+        if (ceil_div(m.pieces, m.lanes) == 1) gn_rows_backward_kernel<T, 1><<<grid, kThreads, 0, p.stream>>>(p, m, part);
+        else gn_rows_backward_kernel<T, 2><<<grid, kThreads, 0, p.stream>>>(p, m, part);
+        if (sums) gn_channel_sum_kernel<<<ceil_div(2ll * p.C, 32), kThreads, 0, p.stream>>>(p, ctas, part);
+        break;
+    }
+    case kFormPositions: {
+        const PositionMap m = position_map(p, K);
+        return m.K == K ? backward_positions<T, K>(p, m) : backward_positions<T, 1>(p, m);
+    }
+    default: {
+        if (sums) {
+            const int k = channel_slices(p);
+            gn_channel_partial_kernel<T><<<dim3(k, ceil_div(p.C, 32)), kThreads, 0, p.stream>>>(p, k, p.scratch);
+            gn_channel_sum_kernel<<<ceil_div(2ll * p.C, 32), kThreads, 0, p.stream>>>(p, k, p.scratch);
+        }
+        if (form_of(p, true) == kFormWide) {
+            gn_wide_backward_kernel<T><<<(unsigned)(p.N * p.G), kThreads, 0, p.stream>>>(p);
+            break;
+        }
+        const TileMap m = tile_map<T>(p);
+        const int most = ceil_div(p.N, m.rows);
+        constexpr int smem = 2 * kTileValues * sizeof(float);
+        const cudaError_t e = cudaFuncSetAttribute(gn_tiles_backward_kernel<T>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        gn_tiles_backward_kernel<T><<<most < 152 * 3 ? most : 152 * 3, kThreads, smem, p.stream>>>(p, m);
+    }
     }
     return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t gn_forward_scratch_bytes(const GroupNorm &) { return 0; }
+size_t gn_forward_scratch_bytes(const GroupNorm &p)
+{
+    if (p.N == 0 || form_of(p, false) != kFormPositions) return 0;
+    const PositionMap m = position_map(p, p.dtype == DP_F32 ? 4 : 8);
+    return (position_part_values(p, m) + 2 * (size_t)p.N * p.G) * sizeof(float);
+}
 
-size_t gn_backward_scratch_bytes(const GroupNorm &p) { return (size_t)channel_slices(p) * 2 * p.C * sizeof(float); }
+size_t gn_backward_scratch_bytes(const GroupNorm &p)
+{
+    if (p.N == 0) return 0;
+    const int vec = p.dtype == DP_F32 ? 4 : 8;
+    switch (form_of(p, true)) {
+    case kFormRows: return (size_t)row_ctas(p, row_map(p, vec), 4) * 2 * p.C * sizeof(float);
+    case kFormPositions:
+        return (position_part_values(p, position_map(p, vec)) + 2 * (size_t)p.N * p.G) * sizeof(float);
+    default: return (size_t)channel_slices(p) * 2 * p.C * sizeof(float);
+    }
+}
 
 cudaError_t launch_gn_forward(const GroupNorm &p)
 {
