@@ -534,20 +534,34 @@ def linear_attention_backward_varlen(q, k, v, log_decay, h0=None, *, cu_seqlens,
 
 
 def _gn_dims(x, weight, bias, groups, act, eps):
-    if x.dim() < 2:
+    shape, dt = x.shape, x.dtype
+    if len(shape) < 2:
         raise ValueError("x must be [N, ..., C]")
-    if act not in _lib.ACTS:
+    code = _lib.ACTS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {sorted(_lib.ACTS)}")
-    _lib._need_cuda("x", x, x.dtype)
-    N, C = x.shape[0], x.shape[-1]
-    S = 1
-    for n in x.shape[1:-1]:
+    _lib._need_cuda("x", x, dt)
+    S, C = 1, shape[-1]
+    for n in shape[1:-1]:
         S *= n
     for name, t in (("weight", weight), ("bias", bias)):
-        _lib._need_cuda(name, t, x.dtype)
-        if t is not None and t.shape != (C,):
-            raise ValueError(f"{name} must be [C]")
-    return _lib.GnDims(N, S, C, int(groups), _lib._dtype_code(x.dtype), _lib.ACTS[act], float(eps))
+        if t is not None:
+            _lib._need_cuda(name, t, dt)
+            if t.shape != (C,):
+                raise ValueError(f"{name} must be [C]")
+    return _lib.GnDims(shape[0], S, C, int(groups), _lib._dtype_code(dt), code, float(eps))
+
+
+def _gn_workspace(workspace, query, dims, device):
+    """(pointer, bytes): the given workspace, or one of the size asked for."""
+    if workspace is None:
+        n = _lib.sized(query, dims)
+        if n == 0:
+            return None, 0, None
+        workspace = torch.empty(n, dtype=torch.uint8, device=device)
+    else:
+        _lib._need_cuda("workspace", workspace)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def group_norm_workspace_size(N, S, C, *, groups, dtype=torch.bfloat16, backward=False):
@@ -570,14 +584,13 @@ def group_norm(x, weight=None, bias=None, *, groups, eps=1e-5, act="none", out=N
     _lib._need_cuda("out", out, x.dtype)
     if out.shape != x.shape:
         raise ValueError("out must have the shape of x")
-    stats = torch.empty((2, dims.N, max(dims.G, 0)), dtype=torch.float32, device=x.device)
-    if workspace is None:
-        workspace = torch.empty(_lib.sized("dp_group_norm_workspace_size", dims), dtype=torch.uint8, device=x.device)
-    _lib._need_cuda("workspace", workspace)
-    p, mean, rstd = _lib._ptr, stats[0], stats[1]
-    _lib._check(_lib.lib().dp_group_norm(dims, p(x), p(weight), p(bias), p(out), p(mean), p(rstd), p(workspace),
-                                         workspace.numel() * workspace.element_size(), _lib._stream(stream)),
-                "dp_group_norm")
+    lead = (dims.N, max(dims.G, 0))
+    mean = torch.empty(lead, dtype=torch.float32, device=x.device)
+    rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
+    ws, size, _keep = _gn_workspace(workspace, "dp_group_norm_workspace_size", dims, x.device)
+    p = _lib._ptr
+    _lib._check(_lib.lib().dp_group_norm(dims, p(x), p(weight), p(bias), p(out), p(mean), p(rstd), ws, size,
+                                         _lib._stream(stream)), "dp_group_norm")
     return out, mean, rstd
 
 
@@ -597,14 +610,10 @@ def group_norm_backward(dy, x, weight, bias, mean, rstd, *, groups, act="none", 
     g = {"dx": torch.empty_like(x)}
     for name, t in (("dweight", weight), ("dbias", bias)):
         g[name] = None if t is None else torch.empty(dims.C, dtype=torch.float32, device=x.device)
-    if workspace is None:
-        workspace = torch.empty(_lib.sized("dp_group_norm_backward_workspace_size", dims), dtype=torch.uint8,
-                                device=x.device)
-    _lib._need_cuda("workspace", workspace)
+    ws, size, _keep = _gn_workspace(workspace, "dp_group_norm_backward_workspace_size", dims, x.device)
     p = _lib._ptr
     _lib._check(_lib.lib().dp_group_norm_backward(dims, p(dy), p(x), p(weight), p(bias), p(mean), p(rstd),
-                                                  p(g["dx"]), p(g["dweight"]), p(g["dbias"]), p(workspace),
-                                                  workspace.numel() * workspace.element_size(),
+                                                  p(g["dx"]), p(g["dweight"]), p(g["dbias"]), ws, size,
                                                   _lib._stream(stream)), "dp_group_norm_backward")
     return g
 

@@ -692,7 +692,13 @@ dp_status make_gn(const dp_gn_dims *d, dp::GroupNorm *p)
     return DP_OK;
 }
 
-size_t gn_workspace(size_t scratch) { return kStatusBlock + ((scratch + 255) & ~(size_t)255); }
+size_t gn_workspace(size_t scratch) { return (scratch + 255) & ~(size_t)255; }
+
+// no workspace is looked at where none is needed
+dp_status check_gn_workspace(const void *workspace, size_t bytes, size_t need)
+{
+    return need == 0 ? DP_OK : check_workspace(workspace, bytes, need);
+}
 
 }  // namespace
 
@@ -729,9 +735,9 @@ dp_status dp_group_norm(const dp_gn_dims *dims, const void *x, const void *weigh
     if (bias) DP_TRY(check_ptr(bias, el));
     if (mean) DP_TRY(check_ptr(mean, 4));
     if (rstd) DP_TRY(check_ptr(rstd, 4));
-    DP_TRY(check_workspace(workspace, workspace_bytes, gn_workspace(dp::gn_forward_scratch_bytes(p))));
+    DP_TRY(check_gn_workspace(workspace, workspace_bytes, gn_workspace(dp::gn_forward_scratch_bytes(p))));
     p.x = x; p.weight = weight; p.bias = bias; p.y = y; p.mean = mean; p.rstd = rstd;
-    p.scratch = (float *)((char *)workspace + kStatusBlock);
+    p.scratch = (float *)workspace;
     p.stream = (cudaStream_t)stream;
     return from_cuda(dp::launch_gn_forward(p));
 }
@@ -753,7 +759,7 @@ dp_status dp_group_norm_backward(const dp_gn_dims *dims, const void *dy, const v
         DP_TRY(check_ptr(rstd, 4));
         if (weight) DP_TRY(check_ptr(weight, el));
         if (bias) DP_TRY(check_ptr(bias, el));
-        DP_TRY(check_workspace(workspace, workspace_bytes, gn_workspace(dp::gn_backward_scratch_bytes(p))));
+        DP_TRY(check_gn_workspace(workspace, workspace_bytes, gn_workspace(dp::gn_backward_scratch_bytes(p))));
     }
     if (p.N == 0) {   // sums over no rows
         for (float *t : {dweight, dbias})
@@ -764,7 +770,7 @@ dp_status dp_group_norm_backward(const dp_gn_dims *dims, const void *dy, const v
     p.x = x; p.weight = weight; p.bias = bias; p.dy = dy; p.dx = dx;
     p.mean = const_cast<float *>(mean); p.rstd = const_cast<float *>(rstd);
     p.dweight = dweight; p.dbias = dbias;
-    p.scratch = (float *)((char *)workspace + kStatusBlock);
+    p.scratch = (float *)workspace;
     p.stream = (cudaStream_t)stream;
     return from_cuda(dp::launch_gn_backward(p));
 }

@@ -19,6 +19,7 @@
 //  wide       S = 1, what is left (very wide groups or rows): a CTA per group.
 // Squared distances are taken from the mean (or summed about a nearby value
 // and combined by counts, means and squares), never as E[x^2] - mean^2.
+#include "f32x2.cuh"
 #include "group_norm.h"
 
 namespace dp {
@@ -70,31 +71,55 @@ template <> struct Piece<__nv_bfloat16, 8> {
 };
 template <typename T> struct Vec { static constexpr int n = 16 / sizeof(T); };
 
-// The sigmoid's exponential and division: exact functions for fp32 results,
-// the hardware approximations (some 2^-21) where the result is rounded to 8
-// bits. sigmoid(z) and 1 - sigmoid(z) from e^-|z|, so that neither cancels.
-template <typename T> __device__ __forceinline__ float act_fwd(float z, int act);
-template <> __device__ __forceinline__ float act_fwd<float>(float z, int act)
+// 16 bytes as pairs of fp32
+template <typename T> __device__ __forceinline__ void widen(uint4 v, uint64_t (&x)[Vec<T>::n / 2]);
+template <> __device__ __forceinline__ void widen<float>(uint4 v, uint64_t (&x)[2])
 {
-    return act == DP_ACT_SILU ? z / (1.f + expf(-z)) : z;
+    x[0] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
+    x[1] = pair(__uint_as_float(v.z), __uint_as_float(v.w));
 }
-template <> __device__ __forceinline__ float act_fwd<__nv_bfloat16>(float z, int act)
+template <> __device__ __forceinline__ void widen<__nv_bfloat16>(uint4 v, uint64_t (&x)[4])
 {
-    return act == DP_ACT_SILU ? __fdividef(z, 1.f + __expf(-z)) : z;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
-template <typename T> __device__ __forceinline__ float exp_neg(float a);
-template <> __device__ __forceinline__ float exp_neg<float>(float a) { return expf(-a); }
-template <> __device__ __forceinline__ float exp_neg<__nv_bfloat16>(float a) { return __expf(-a); }
-template <typename T> __device__ __forceinline__ float recip(float a);
-template <> __device__ __forceinline__ float recip<float>(float a) { return 1.f / a; }
-template <> __device__ __forceinline__ float recip<__nv_bfloat16>(float a) { return __fdividef(1.f, a); }
-// act'(z); SiLU: p (1 + z (1 - p)) with p = sigmoid(z)
-template <typename T> __device__ __forceinline__ float act_grad(float z, int act)
+
+// sigmoid(z): the exact functions for fp32 results, the hardware's exponential
+// and reciprocal (2^-22 each) where the result is rounded to 8 bits. An
+// exponential that overflows gives 0.
+template <typename T> __device__ __forceinline__ float sigmoid(float z);
+template <> __device__ __forceinline__ float sigmoid<float>(float z) { return 1.f / (1.f + expf(-z)); }
+template <> __device__ __forceinline__ float sigmoid<__nv_bfloat16>(float z)
 {
-    if (act != DP_ACT_SILU) return 1.f;
-    const float e = exp_neg<T>(fabsf(z)), r = recip<T>(1.f + e);
-    const float p = z >= 0.f ? r : e * r, m = z >= 0.f ? e * r : r;
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
+template <typename T, int ACT> __device__ __forceinline__ float act_fwd(float z)
+{
+    return ACT == DP_ACT_SILU ? z * sigmoid<T>(z) : z;
+}
+// act'(z); SiLU: p (1 + z (1 - p)) with p = sigmoid(z). For large z, 1 - p is
+// p's rounding, and z (1 - p) below 2^-17 beside 1: in fp32 1 - p is taken as
+// sigmoid(-z), which does not cancel.
+template <typename T, int ACT> __device__ __forceinline__ float act_grad(float z)
+{
+    if (ACT != DP_ACT_SILU) return 1.f;
+    const float p = sigmoid<T>(z);
+    const float m = sizeof(T) == 4 ? sigmoid<T>(-z) : 1.f - p;
     return p * fmaf(z, m, 1.f);
+}
+
+// act'(z) of a pair
+template <typename T, int ACT> __device__ __forceinline__ uint64_t act_grad2(uint64_t z)
+{
+    float a, b;
+    unpair(z, a, b);
+    if (ACT != DP_ACT_SILU || sizeof(T) == 4) return pair(act_grad<T, ACT>(a), act_grad<T, ACT>(b));
+    const uint64_t one = pair(1.f, 1.f), p = pair(sigmoid<T>(a), sigmoid<T>(b));
+    return mul2(p, fma2(z, fma2(p, pair(-1.f, -1.f), one), one));
 }
 
 // sum over the `lanes` (a power of two) neighbouring lanes of a group
@@ -126,166 +151,208 @@ __device__ __forceinline__ float2 block_sum(float a, float b)
 // A row's groups take `lanes` lanes each (the power of two that holds their
 // pieces, or 32 with V pieces a lane); a thread keeps its channels for all the
 // rows it walks, so weights stay in registers, and the gradients' channel
-// sums too. kRows rows are in flight at once.
+// sums too. Two pieces a lane where a group has them (forward): half the
+// steps of the lanes' sums for each value.
 struct RowMap {
     int lanes, pieces;      // of a group
     int slots, per;         // lanes of a row; rows that a CTA takes at once (1 if the row needs several CTAs)
 };
 
-RowMap row_map(const GroupNorm &p, int vec)
+RowMap row_map(const GroupNorm &p, int vec, int each)
 {
     RowMap m;
     m.pieces = p.C / p.G / vec;
     m.lanes = 1;
-    while (m.lanes < m.pieces && m.lanes < 32) m.lanes *= 2;
+    while (m.lanes * each < m.pieces && m.lanes < 32) m.lanes *= 2;
     m.slots = p.G * m.lanes;
     m.per = m.slots < kThreads ? kThreads / m.slots : 1;
     return m;
 }
 
-template <typename T, int V>
+template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(kThreads)
 gn_rows_kernel(GroupNorm p, RowMap m)
 {
-    constexpr int K = Vec<T>::n, kRows = V == 1 ? 2 : 1;
+    constexpr int K = Vec<T>::n, H = K / 2;
     const int W = p.C / p.G;
     const int slot = m.per > 1 ? threadIdx.x % m.slots : blockIdx.y * kThreads + threadIdx.x;
     const int sub = m.per > 1 ? threadIdx.x / m.slots : 0;
     const bool in = sub < m.per && slot < m.slots;
     const int g = in ? slot / m.lanes : 0, l = slot & (m.lanes - 1);
     const float inv = 1.f / (float)W;
-    float w[V][K], b[V][K];
+    uint64_t w[V][H], b[V][H];
     bool on[V];
     size_t at[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         on[v] = in && l + v * m.lanes < m.pieces;
         at[v] = (size_t)g * W + (size_t)(l + v * m.lanes) * K;
+        float wf[K], bf[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            w[v][k] = 1.f;
-            b[v][k] = 0.f;
+            wf[k] = 1.f;
+            bf[k] = 0.f;
         }
-        if (on[v] && p.weight) Piece<T, K>::load((const T *)p.weight + at[v], w[v]);
-        if (on[v] && p.bias) Piece<T, K>::load((const T *)p.bias + at[v], b[v]);
+        if (on[v] && p.weight) Piece<T, K>::load((const T *)p.weight + at[v], wf);
+        if (on[v] && p.bias) Piece<T, K>::load((const T *)p.bias + at[v], bf);
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+            w[v][k] = pair(wf[2 * k], wf[2 * k + 1]);
+            b[v][k] = pair(bf[2 * k], bf[2 * k + 1]);
+        }
     }
     const long long step = (long long)gridDim.x * m.per;
+    uint4 next[V];
+    const auto fetch = [&](long long n) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            next[v] = make_uint4(0, 0, 0, 0);
+            if (on[v] && n < p.N) next[v] = *(const uint4 *)((const T *)p.x + (size_t)n * p.C + at[v]);
+        }
+    };
+    fetch((long long)blockIdx.x * m.per + sub);
     // every thread of a warp makes the same number of turns (the lanes' sums)
-    for (long long n0 = (long long)blockIdx.x * m.per; n0 < p.N; n0 += step * kRows) {
-        float x[kRows][V][K];
+    for (long long n0 = (long long)blockIdx.x * m.per; n0 < p.N; n0 += step) {
+        const long long n = n0 + sub;
+        const bool row = n < p.N;
+        uint64_t x[V][H], sum = 0, sq = 0;       // 0: two fp32 zeros
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
+        for (int v = 0; v < V; ++v) widen<T>(next[v], x[v]);
+        fetch(n + step);                         // on its way during this row
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
+        for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int k = 0; k < K; ++k) x[r][v][k] = 0.f;
-                const long long n = n0 + r * step + sub;
-                if (on[v] && n < p.N) Piece<T, K>::load((const T *)p.x + (size_t)n * p.C + at[v], x[r][v]);
-            }
+            for (int k = 0; k < H; ++k) sum = add2(sum, x[v][k]);
+        float s0, s1;
+        unpair(sum, s0, s1);
+        const float mean = lane_sum(s0 + s1, m.lanes) * inv;
+        const uint64_t off = pair(-mean, -mean);
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            const long long n = n0 + r * step + sub;
-            float sum = 0.f, sq = 0.f;
+        for (int v = 0; v < V; ++v)
+            if (on[v])
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int k = 0; k < K; ++k) sum += x[r][v][k];
-            const float mean = lane_sum(sum, m.lanes) * inv;
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (on[v])
-#pragma unroll
-                    for (int k = 0; k < K; ++k) {
-                        x[r][v][k] -= mean;
-                        sq = fmaf(x[r][v][k], x[r][v][k], sq);
-                    }
-            const float rstd = 1.f / sqrtf(fmaf(lane_sum(sq, m.lanes), inv, p.eps));
-            if (n >= p.N) continue;
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (on[v]) {
-#pragma unroll
-                    for (int k = 0; k < K; ++k)
-                        x[r][v][k] = act_fwd<T>(fmaf(x[r][v][k] * rstd, w[v][k], b[v][k]), p.act);
-                    Piece<T, K>::store((T *)p.y + (size_t)n * p.C + at[v], x[r][v]);
+                for (int k = 0; k < H; ++k) {
+                    x[v][k] = add2(x[v][k], off);
+                    sq = fma2(x[v][k], x[v][k], sq);
                 }
-            if (in && l == 0) {
-                if (p.mean) p.mean[n * p.G + g] = mean;
-                if (p.rstd) p.rstd[n * p.G + g] = rstd;
+        unpair(sq, s0, s1);
+        const float rstd = 1.f / sqrtf(fmaf(lane_sum(s0 + s1, m.lanes), inv, p.eps));
+        if (!row) continue;
+        const uint64_t rr = pair(rstd, rstd);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (on[v]) {
+                float f[K];
+#pragma unroll
+                for (int k = 0; k < H; ++k) {
+                    unpair(fma2(mul2(x[v][k], rr), w[v][k], b[v][k]), f[2 * k], f[2 * k + 1]);
+                    f[2 * k] = act_fwd<T, ACT>(f[2 * k]);
+                    f[2 * k + 1] = act_fwd<T, ACT>(f[2 * k + 1]);
+                }
+                Piece<T, K>::store((T *)p.y + (size_t)n * p.C + at[v], f);
             }
+        if (in && l == 0) {
+            if (p.mean) p.mean[n * p.G + g] = mean;
+            if (p.rstd) p.rstd[n * p.G + g] = rstd;
         }
     }
 }
 
 // Channel sums of the gradients leave each CTA as one row of partial sums
 // [slice][2][C]; gn_channel_sum_kernel adds the rows in order.
-template <typename T, int V>
+template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(kThreads)
 gn_rows_backward_kernel(GroupNorm p, RowMap m, float *part)
 {
     constexpr int K = Vec<T>::n;
     __shared__ float red[kThreads * (K + 1)];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int W = p.C / p.G;
     const int slot = m.per > 1 ? threadIdx.x % m.slots : blockIdx.y * kThreads + threadIdx.x;
     const int sub = m.per > 1 ? threadIdx.x / m.slots : 0;
     const bool in = sub < m.per && slot < m.slots;
     const int g = in ? slot / m.lanes : 0, l = slot & (m.lanes - 1);
     const float inv = 1.f / (float)W;
-    float w[V][K], b[V][K], dw[V][K], db[V][K];
+    constexpr int H = K / 2;
+    uint64_t w[V][H], b[V][H], dw[V][H], db[V][H];
     bool on[V];
     size_t at[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         on[v] = in && l + v * m.lanes < m.pieces;
         at[v] = (size_t)g * W + (size_t)(l + v * m.lanes) * K;
+        float wf[K], bf[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            w[v][k] = 1.f;
-            b[v][k] = dw[v][k] = db[v][k] = 0.f;
+            wf[k] = 1.f;
+            bf[k] = 0.f;
         }
-        if (on[v] && p.weight) Piece<T, K>::load((const T *)p.weight + at[v], w[v]);
-        if (on[v] && p.bias) Piece<T, K>::load((const T *)p.bias + at[v], b[v]);
+        if (on[v] && p.weight) Piece<T, K>::load((const T *)p.weight + at[v], wf);
+        if (on[v] && p.bias) Piece<T, K>::load((const T *)p.bias + at[v], bf);
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+            w[v][k] = pair(wf[2 * k], wf[2 * k + 1]);
+            b[v][k] = pair(bf[2 * k], bf[2 * k + 1]);
+            dw[v][k] = db[v][k] = 0;
+        }
     }
     const long long step = (long long)gridDim.x * m.per;
+    uint4 nx[V], nd[V];
+    float nmean = 0.f, nrstd = 0.f;
+    const auto fetch = [&](long long n) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            nx[v] = nd[v] = make_uint4(0, 0, 0, 0);
+            if (on[v] && n < p.N) {
+                nx[v] = *(const uint4 *)((const T *)p.x + (size_t)n * p.C + at[v]);
+                nd[v] = *(const uint4 *)((const T *)p.dy + (size_t)n * p.C + at[v]);
+            }
+        }
+        if (in && n < p.N) {
+            nmean = p.mean[n * p.G + g];
+            nrstd = p.rstd[n * p.G + g];
+        }
+    };
+    fetch((long long)blockIdx.x * m.per + sub);
     for (long long n0 = (long long)blockIdx.x * m.per; n0 < p.N; n0 += step) {
         const long long n = n0 + sub;
         const bool row = n < p.N;
-        float h[V][K], u[V][K], mean = 0.f, rstd = 0.f;
-        if (in && row) {
-            mean = p.mean[n * p.G + g];
-            rstd = p.rstd[n * p.G + g];
-        }
+        uint64_t h[V][H], u[V][H], su = 0, suh = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-#pragma unroll
-            for (int k = 0; k < K; ++k) h[v][k] = u[v][k] = 0.f;
-            if (on[v] && row) {
-                Piece<T, K>::load((const T *)p.x + (size_t)n * p.C + at[v], h[v]);
-                Piece<T, K>::load((const T *)p.dy + (size_t)n * p.C + at[v], u[v]);
-            }
+            widen<T>(nx[v], h[v]);
+            widen<T>(nd[v], u[v]);
         }
-        float su = 0.f, suh = 0.f;
+        const float rstd = nrstd;
+        const uint64_t off = pair(-nmean, -nmean), rr = pair(rstd, rstd);
+        fetch(n + step);
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (on[v] && row)
 #pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    const float hh = (h[v][k] - mean) * rstd;
-                    const float d = u[v][k] * act_grad<T>(fmaf(hh, w[v][k], b[v][k]), p.act);
-                    dw[v][k] = fmaf(d, hh, dw[v][k]);
-                    db[v][k] += d;
-                    h[v][k] = hh;
-                    u[v][k] = d * w[v][k];
-                    su += u[v][k];
-                    suh = fmaf(u[v][k], hh, suh);
+                for (int k = 0; k < H; ++k) {
+                    h[v][k] = mul2(add2(h[v][k], off), rr);
+                    const uint64_t d = mul2(u[v][k], act_grad2<T, ACT>(fma2(h[v][k], w[v][k], b[v][k])));
+                    dw[v][k] = fma2(d, h[v][k], dw[v][k]);
+                    db[v][k] = add2(db[v][k], d);
+                    u[v][k] = mul2(d, w[v][k]);
+                    su = add2(su, u[v][k]);
+                    suh = fma2(u[v][k], h[v][k], suh);
                 }
-        const float mu = lane_sum(su, m.lanes) * inv, muh = lane_sum(suh, m.lanes) * inv;
+        float s0, s1;
+        unpair(su, s0, s1);
+        const float mu = lane_sum(s0 + s1, m.lanes) * inv;
+        unpair(suh, s0, s1);
+        const float muh = lane_sum(s0 + s1, m.lanes) * inv;
+        const uint64_t a = pair(-mu, -mu), c = pair(-muh, -muh);
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (on[v] && row) {
+                float f[K];
 #pragma unroll
-                for (int k = 0; k < K; ++k) u[v][k] = rstd * (u[v][k] - mu - h[v][k] * muh);
-                Piece<T, K>::store((T *)p.dx + (size_t)n * p.C + at[v], u[v]);
+                for (int k = 0; k < H; ++k)
+                    unpair(mul2(fma2(h[v][k], c, add2(u[v][k], a)), rr), f[2 * k], f[2 * k + 1]);
+                Piece<T, K>::store((T *)p.dx + (size_t)n * p.C + at[v], f);
             }
     }
     if (!part) return;
@@ -296,7 +363,9 @@ gn_rows_backward_kernel(GroupNorm p, RowMap m, float *part)
         for (int v = 0; v < V; ++v) {
             __syncthreads();
 #pragma unroll
-            for (int k = 0; k < K; ++k) red[threadIdx.x * (K + 1) + k] = which ? db[v][k] : dw[v][k];
+            for (int k = 0; k < H; ++k)
+                unpair(which ? db[v][k] : dw[v][k], red[threadIdx.x * (K + 1) + 2 * k],
+                       red[threadIdx.x * (K + 1) + 2 * k + 1]);
             __syncthreads();
             if (sub == 0 && on[v]) {
                 float *dst = part + ((size_t)blockIdx.x * 2 + which) * p.C + at[v];
@@ -310,24 +379,26 @@ gn_rows_backward_kernel(GroupNorm p, RowMap m, float *part)
         }
 }
 
-// one warp per channel sum: lanes over the slices, then across the lanes in a
-// fixed tree
-__global__ void __launch_bounds__(kThreads)
+// A CTA adds 32 neighbouring entries of [2][C]: its warps take every 32nd
+// slice, then one warp adds the warps' sums, always in the same order.
+constexpr int kSumThreads = 1024;
+__global__ void __launch_bounds__(kSumThreads)
 gn_channel_sum_kernel(GroupNorm p, int slices, const float *part)
 {
-    __shared__ float red[kThreads / 32][33];
-    // a CTA adds 32 neighbouring entries of [2][C]; warp = every 8th slice
+    __shared__ float red[kSumThreads / 32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long i = (long long)blockIdx.x * 32 + lane;
     float s = 0.f;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (i < 2ll * p.C)
-        for (int k = warp; k < slices; k += kThreads / 32) s += part[(size_t)k * 2 * p.C + i];
+#pragma unroll 8
+        for (int k = warp; k < slices; k += kSumThreads / 32) s += part[(size_t)k * 2 * p.C + i];
     red[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && i < 2ll * p.C) {
         s = 0.f;
 #pragma unroll
-        for (int k = 0; k < kThreads / 32; ++k) s += red[k][lane];
+        for (int k = 0; k < kSumThreads / 32; ++k) s += red[k][lane];
         float *dst = i < p.C ? p.dweight : p.dbias;
         if (dst) dst[i < p.C ? i : i - p.C] = s;
     }
@@ -382,7 +453,7 @@ __device__ __forceinline__ void tile_out(T *dst, const float *src, size_t at, in
     for (int i = whole * K + threadIdx.x; i < count; i += kThreads) st(dst, at + i, src[i]);
 }
 
-template <typename T>
+template <typename T, int ACT>
 __global__ void __launch_bounds__(kThreads)
 gn_tiles_kernel(GroupNorm p, TileMap m)
 {
@@ -410,7 +481,7 @@ gn_tiles_kernel(GroupNorm p, TileMap m)
                 float z = (x[i] - mean) * rstd;
                 if (p.weight) z *= ld((const T *)p.weight, c0 + i);
                 if (p.bias) z += ld((const T *)p.bias, c0 + i);
-                x[i] = act_fwd<T>(z, p.act);
+                x[i] = act_fwd<T, ACT>(z);
             }
             if (l == 0) {
                 if (p.mean) p.mean[n0 * p.G + q] = mean;
@@ -422,7 +493,7 @@ gn_tiles_kernel(GroupNorm p, TileMap m)
     }
 }
 
-template <typename T>
+template <typename T, int ACT>
 __global__ void __launch_bounds__(kThreads)
 gn_tiles_backward_kernel(GroupNorm p, TileMap m)
 {
@@ -446,7 +517,7 @@ gn_tiles_backward_kernel(GroupNorm p, TileMap m)
                 for (int i = l; i < W; i += m.lanes) {
                     const float h = (x[i] - mean) * rstd, w = p.weight ? ld((const T *)p.weight, c0 + i) : 1.f;
                     const float z = fmaf(h, w, p.bias ? ld((const T *)p.bias, c0 + i) : 0.f);
-                    const float u = d[i] * act_grad<T>(z, p.act) * w;
+                    const float u = d[i] * act_grad<T, ACT>(z) * w;
                     x[i] = h;
                     d[i] = u;
                     su += u;
@@ -464,7 +535,7 @@ gn_tiles_backward_kernel(GroupNorm p, TileMap m)
 // ---------------------------------------------------------------- wide
 // One CTA per (sample, group): the mean, the squared distances from it, the
 // outputs, each in a walk over the group's values.
-template <typename T>
+template <typename T, int ACT>
 __global__ void __launch_bounds__(kThreads)
 gn_wide_kernel(GroupNorm p)
 {
@@ -489,21 +560,21 @@ gn_wide_kernel(GroupNorm p)
         float z = (ld(x, base + i) - mean) * rstd;
         if (w) z *= ld(w, (size_t)g * W + i);
         if (b) z += ld(b, (size_t)g * W + i);
-        st(y, base + i, act_fwd<T>(z, p.act));
+        st(y, base + i, act_fwd<T, ACT>(z));
     }
 }
 
-template <typename T>
+template <typename T, int ACT>
 __device__ __forceinline__ float2 grad_of(const GroupNorm &p, size_t i, int c, float mean, float rstd)
 {
     const float h = (ld((const T *)p.x, i) - mean) * rstd;
     float z = h;
     if (p.weight) z *= ld((const T *)p.weight, c);
     if (p.bias) z += ld((const T *)p.bias, c);
-    return make_float2(ld((const T *)p.dy, i) * act_grad<T>(z, p.act), h);
+    return make_float2(ld((const T *)p.dy, i) * act_grad<T, ACT>(z), h);
 }
 
-template <typename T>
+template <typename T, int ACT>
 __global__ void __launch_bounds__(kThreads)
 gn_wide_backward_kernel(GroupNorm p)
 {
@@ -512,7 +583,7 @@ gn_wide_backward_kernel(GroupNorm p)
     const float mean = p.mean[blockIdx.x], rstd = p.rstd[blockIdx.x];
     const auto u_of = [&](int i, float &h) {
         const int c = g * W + i;
-        const float2 dh = grad_of<T>(p, base + i, c, mean, rstd);
+        const float2 dh = grad_of<T, ACT>(p, base + i, c, mean, rstd);
         h = dh.y;
         return p.weight ? dh.x * ld((const T *)p.weight, c) : dh.x;
     };
@@ -533,7 +604,7 @@ gn_wide_backward_kernel(GroupNorm p)
 
 // Channel sums for the tile and wide forms: a CTA adds the rows of its slice
 // for 32 channels. (dx is written after, where it may lie over dy.)
-template <typename T>
+template <typename T, int ACT>
 __global__ void __launch_bounds__(kThreads)
 gn_channel_partial_kernel(GroupNorm p, int slices, float *part)
 {
@@ -546,7 +617,7 @@ gn_channel_partial_kernel(GroupNorm p, int slices, float *part)
         const int g = c / (p.C / p.G);
         for (long long r = r0 + warp; r < r1; r += kThreads / 32) {
             const size_t ng = (size_t)r * p.G + g;
-            const float2 dh = grad_of<T>(p, (size_t)r * p.C + c, c, p.mean[ng], p.rstd[ng]);
+            const float2 dh = grad_of<T, ACT>(p, (size_t)r * p.C + c, c, p.mean[ng], p.rstd[ng]);
             dw = fmaf(dh.x, dh.y, dw);
             db += dh.x;
         }
@@ -579,8 +650,8 @@ PositionMap position_map(const GroupNorm &p, int vec)
     m.cols = pieces < kThreads ? pieces : kThreads;
     m.rows = kThreads / m.cols;
     m.blocks = (pieces + m.cols - 1) / m.cols;
-    // about two CTAs for each of the SMs, and at least four turns for each
-    const long long want = (2 * 152 + p.N * m.blocks - 1) / (p.N * m.blocks);
+    // about four CTAs for each of the SMs, and at least four turns for each
+    const long long want = (4 * 152 + p.N * m.blocks - 1) / (p.N * m.blocks);
     const long long most = (p.S + 4 * m.rows - 1) / (4 * m.rows);
     m.slices = (int)(want < most ? want : most);
     if (m.slices < 1) m.slices = 1;
@@ -683,6 +754,25 @@ gn_position_combine_kernel(GroupNorm p, PositionMap m, const float *part, float 
     }
 }
 
+// d = dy act'(z) and h of K values of one row, in place of dy and x
+template <typename T, int K, int ACT>
+__device__ __forceinline__ void grads(float (&x)[K], float (&d)[K], const float (&mean)[K], const float (&rstd)[K],
+                                      const float (&w)[K], const float (&b)[K])
+{
+    if constexpr (K == 1) {
+        x[0] = (x[0] - mean[0]) * rstd[0];
+        d[0] *= act_grad<T, ACT>(fmaf(x[0], w[0], b[0]));
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; k += 2) {
+            const uint64_t h = mul2(pair(x[k] - mean[k], x[k + 1] - mean[k + 1]), pair(rstd[k], rstd[k + 1]));
+            const uint64_t g = act_grad2<T, ACT>(fma2(h, pair(w[k], w[k + 1]), pair(b[k], b[k + 1])));
+            unpair(h, x[k], x[k + 1]);
+            unpair(mul2(pair(d[k], d[k + 1]), g), d[k], d[k + 1]);
+        }
+    }
+}
+
 // what a thread holds of its channels
 template <typename T, int K> struct Channels {
     float w[K], b[K], mean[K], rstd[K];
@@ -700,7 +790,7 @@ template <typename T, int K> struct Channels {
     }
 };
 
-template <typename T, int K>
+template <typename T, int K, int ACT>
 __global__ void __launch_bounds__(kThreads)
 gn_position_apply_kernel(GroupNorm p, PositionMap m, const float *mean, const float *rstd)
 {
@@ -720,14 +810,14 @@ gn_position_apply_kernel(GroupNorm p, PositionMap m, const float *mean, const fl
         Piece<T, K>::load((const T *)p.x + at + (size_t)s * p.C, f);
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            f[k] = act_fwd<T>(fmaf((f[k] - ch.mean[k]) * ch.rstd[k], ch.w[k], ch.b[k]), p.act);
+            f[k] = act_fwd<T, ACT>(fmaf((f[k] - ch.mean[k]) * ch.rstd[k], ch.w[k], ch.b[k]));
         Piece<T, K>::store((T *)p.y + at + (size_t)s * p.C, f);
     }
 }
 
 // per channel of a slice: sums of d h and of d, which are both the gradients'
 // channel sums and, weighted, the groups' sums of u h and u
-template <typename T, int K>
+template <typename T, int K, int ACT>
 __global__ void __launch_bounds__(kThreads)
 gn_position_grad_kernel(GroupNorm p, PositionMap m, float *part)
 {
@@ -751,12 +841,11 @@ gn_position_grad_kernel(GroupNorm p, PositionMap m, float *part)
             float x[K], d[K];
             Piece<T, K>::load((const T *)p.x + at + (size_t)s * p.C, x);
             Piece<T, K>::load((const T *)p.dy + at + (size_t)s * p.C, d);
+            grads<T, K, ACT>(x, d, ch.mean, ch.rstd, ch.w, ch.b);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const float h = (x[k] - ch.mean[k]) * ch.rstd[k];
-                const float dd = d[k] * act_grad<T>(fmaf(h, ch.w[k], ch.b[k]), p.act);
-                a[k] = fmaf(dd, h, a[k]);
-                q[k] += dd;
+                a[k] = fmaf(d[k], x[k], a[k]);
+                q[k] += d[k];
             }
         }
 #pragma unroll
@@ -799,7 +888,7 @@ gn_position_grad_combine_kernel(GroupNorm p, PositionMap m, const float *part, f
     if (threadIdx.x == 0) sums[blockIdx.x] = make_float2(s.x * inv, s.y * inv);
 }
 
-template <typename T, int K>
+template <typename T, int K, int ACT>
 __global__ void __launch_bounds__(kThreads)
 gn_position_dx_kernel(GroupNorm p, PositionMap m, const float2 *sums)
 {
@@ -826,12 +915,9 @@ gn_position_dx_kernel(GroupNorm p, PositionMap m, const float2 *sums)
         float x[K], d[K];
         Piece<T, K>::load((const T *)p.x + at + (size_t)s * p.C, x);
         Piece<T, K>::load((const T *)p.dy + at + (size_t)s * p.C, d);
+        grads<T, K, ACT>(x, d, ch.mean, ch.rstd, ch.w, ch.b);
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const float h = (x[k] - ch.mean[k]) * ch.rstd[k];
-            const float u = d[k] * act_grad<T>(fmaf(h, ch.w[k], ch.b[k]), p.act) * ch.w[k];
-            d[k] = ch.rstd[k] * (u - mu[k] - h * muh[k]);
-        }
+        for (int k = 0; k < K; ++k) d[k] = ch.rstd[k] * (fmaf(d[k], ch.w[k], -mu[k]) - x[k] * muh[k]);
         Piece<T, K>::store((T *)p.dx + at + (size_t)s * p.C, d);
     }
 }
@@ -867,12 +953,14 @@ int channel_slices(const GroupNorm &p)
 
 size_t position_part_values(const GroupNorm &p, const PositionMap &m) { return (size_t)p.N * m.slices * 2 * p.C; }
 
+// A kernel that may start while the one before it finishes (it waits for that
+// one's results itself).
 template <typename... A, typename... B>
-cudaError_t launch_after(void (*kernel)(A...), dim3 grid, cudaStream_t stream, B... args)
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, cudaStream_t stream, B... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -882,7 +970,12 @@ cudaError_t launch_after(void (*kernel)(A...), dim3 grid, cudaStream_t stream, B
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <typename T, int K>
+cudaError_t channel_sum(const GroupNorm &p, int slices, const float *part)
+{
+    return launch_after(gn_channel_sum_kernel, dim3(ceil_div(2ll * p.C, 32)), kSumThreads, p.stream, p, slices, part);
+}
+
+template <typename T, int K, int ACT>
 cudaError_t forward_positions(const GroupNorm &p, const PositionMap &m)
 {
     const dim3 grid((unsigned)(p.N * m.slices), m.blocks);
@@ -890,94 +983,94 @@ cudaError_t forward_positions(const GroupNorm &p, const PositionMap &m)
     if (!mean) mean = part + position_part_values(p, m);
     if (!rstd) rstd = part + position_part_values(p, m) + (size_t)p.N * p.G;
     gn_position_stats_kernel<T, K><<<grid, kThreads, 0, p.stream>>>(p, m, part);
-    cudaError_t e = launch_after(gn_position_combine_kernel, dim3((unsigned)(p.N * p.G)), p.stream, p, m,
+    cudaError_t e = launch_after(gn_position_combine_kernel, dim3((unsigned)(p.N * p.G)), kThreads, p.stream, p, m,
                                  (const float *)part, mean, rstd);
     if (e != cudaSuccess) return e;
-    return launch_after(gn_position_apply_kernel<T, K>, grid, p.stream, p, m, (const float *)mean, (const float *)rstd);
+    return launch_after(gn_position_apply_kernel<T, K, ACT>, grid, kThreads, p.stream, p, m, (const float *)mean, (const float *)rstd);
 }
 
-template <typename T, int K>
+template <typename T, int K, int ACT>
 cudaError_t backward_positions(const GroupNorm &p, const PositionMap &m)
 {
     const dim3 grid((unsigned)(p.N * m.slices), m.blocks);
     float *part = p.scratch;
     float2 *sums = (float2 *)(part + position_part_values(p, m));
-    gn_position_grad_kernel<T, K><<<grid, kThreads, 0, p.stream>>>(p, m, part);
-    cudaError_t e = launch_after(gn_position_grad_combine_kernel<T>, dim3((unsigned)(p.N * p.G)), p.stream, p, m,
+    gn_position_grad_kernel<T, K, ACT><<<grid, kThreads, 0, p.stream>>>(p, m, part);
+    cudaError_t e = launch_after(gn_position_grad_combine_kernel<T>, dim3((unsigned)(p.N * p.G)), kThreads, p.stream, p, m,
                                  (const float *)part, sums);
     if (e != cudaSuccess) return e;
-    e = launch_after(gn_position_dx_kernel<T, K>, grid, p.stream, p, m, (const float2 *)sums);
+    e = launch_after(gn_position_dx_kernel<T, K, ACT>, grid, kThreads, p.stream, p, m, (const float2 *)sums);
     if (e != cudaSuccess || !(p.dweight || p.dbias)) return e;
-    gn_channel_sum_kernel<<<ceil_div(2ll * p.C, 32), kThreads, 0, p.stream>>>(p, (int)(p.N * m.slices), part);
-    return cudaGetLastError();
+    return channel_sum(p, (int)(p.N * m.slices), part);
 }
 
-template <typename T>
+template <typename T, int ACT>
 cudaError_t forward_typed(const GroupNorm &p)
 {
     constexpr int K = Vec<T>::n;
     switch (form_of(p, false)) {
     case kFormRows: {
-        const RowMap m = row_map(p, K);
+        const RowMap m = row_map(p, K, 2);
         const dim3 grid(row_ctas(p, m, 8), m.per > 1 ? 1 : ceil_div(m.slots, kThreads));
         const int v = ceil_div(m.pieces, m.lanes);
-        if (v == 1) gn_rows_kernel<T, 1><<<grid, kThreads, 0, p.stream>>>(p, m);
-        else if (v == 2) gn_rows_kernel<T, 2><<<grid, kThreads, 0, p.stream>>>(p, m);
-        else gn_rows_kernel<T, 4><<<grid, kThreads, 0, p.stream>>>(p, m);
+        if (v == 1) gn_rows_kernel<T, 1, ACT><<<grid, kThreads, 0, p.stream>>>(p, m);
+        else if (v == 2) gn_rows_kernel<T, 2, ACT><<<grid, kThreads, 0, p.stream>>>(p, m);
+        else gn_rows_kernel<T, 4, ACT><<<grid, kThreads, 0, p.stream>>>(p, m);
         break;
     }
     case kFormTiles: {
         const TileMap m = tile_map<T>(p);
         const int most = ceil_div(p.N, m.rows);
-        gn_tiles_kernel<T><<<most < 152 * 6 ? most : 152 * 6, kThreads, kTileValues * sizeof(float), p.stream>>>(p, m);
+        gn_tiles_kernel<T, ACT><<<most < 152 * 6 ? most : 152 * 6, kThreads, kTileValues * sizeof(float), p.stream>>>(p, m);
         break;
     }
     case kFormPositions: {
         const PositionMap m = position_map(p, K);
-        return m.K == K ? forward_positions<T, K>(p, m) : forward_positions<T, 1>(p, m);
+        return m.K == K ? forward_positions<T, K, ACT>(p, m) : forward_positions<T, 1, ACT>(p, m);
     }
-    default: gn_wide_kernel<T><<<(unsigned)(p.N * p.G), kThreads, 0, p.stream>>>(p);
+    default: gn_wide_kernel<T, ACT><<<(unsigned)(p.N * p.G), kThreads, 0, p.stream>>>(p);
     }
     return cudaGetLastError();
 }
 
-template <typename T>
+template <typename T, int ACT>
 cudaError_t backward_typed(const GroupNorm &p)
 {
     constexpr int K = Vec<T>::n;
     const bool sums = p.dweight || p.dbias;
     switch (form_of(p, true)) {
     case kFormRows: {
-        const RowMap m = row_map(p, K);
+        const RowMap m = row_map(p, K, 1);
         const int ctas = row_ctas(p, m, 4);
         const dim3 grid(ctas, m.per > 1 ? 1 : ceil_div(m.slots, kThreads));
         float *part = sums ? p.scratch : nullptr;
-        if (ceil_div(m.pieces, m.lanes) == 1) gn_rows_backward_kernel<T, 1><<<grid, kThreads, 0, p.stream>>>(p, m, part);
-        else gn_rows_backward_kernel<T, 2><<<grid, kThreads, 0, p.stream>>>(p, m, part);
-        if (sums) gn_channel_sum_kernel<<<ceil_div(2ll * p.C, 32), kThreads, 0, p.stream>>>(p, ctas, part);
+        if (ceil_div(m.pieces, m.lanes) == 1) gn_rows_backward_kernel<T, 1, ACT><<<grid, kThreads, 0, p.stream>>>(p, m, part);
+        else gn_rows_backward_kernel<T, 2, ACT><<<grid, kThreads, 0, p.stream>>>(p, m, part);
+        if (sums) return channel_sum(p, ctas, part);
         break;
     }
     case kFormPositions: {
         const PositionMap m = position_map(p, K);
-        return m.K == K ? backward_positions<T, K>(p, m) : backward_positions<T, 1>(p, m);
+        return m.K == K ? backward_positions<T, K, ACT>(p, m) : backward_positions<T, 1, ACT>(p, m);
     }
     default: {
         if (sums) {
             const int k = channel_slices(p);
-            gn_channel_partial_kernel<T><<<dim3(k, ceil_div(p.C, 32)), kThreads, 0, p.stream>>>(p, k, p.scratch);
-            gn_channel_sum_kernel<<<ceil_div(2ll * p.C, 32), kThreads, 0, p.stream>>>(p, k, p.scratch);
+            gn_channel_partial_kernel<T, ACT><<<dim3(k, ceil_div(p.C, 32)), kThreads, 0, p.stream>>>(p, k, p.scratch);
+            const cudaError_t e = channel_sum(p, k, p.scratch);
+            if (e != cudaSuccess) return e;
         }
         if (form_of(p, true) == kFormWide) {
-            gn_wide_backward_kernel<T><<<(unsigned)(p.N * p.G), kThreads, 0, p.stream>>>(p);
+            gn_wide_backward_kernel<T, ACT><<<(unsigned)(p.N * p.G), kThreads, 0, p.stream>>>(p);
             break;
         }
         const TileMap m = tile_map<T>(p);
         const int most = ceil_div(p.N, m.rows);
         constexpr int smem = 2 * kTileValues * sizeof(float);
-        const cudaError_t e = cudaFuncSetAttribute(gn_tiles_backward_kernel<T>,
+        const cudaError_t e = cudaFuncSetAttribute(gn_tiles_backward_kernel<T, ACT>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        gn_tiles_backward_kernel<T><<<most < 152 * 3 ? most : 152 * 3, kThreads, smem, p.stream>>>(p, m);
+        gn_tiles_backward_kernel<T, ACT><<<most < 152 * 3 ? most : 152 * 3, kThreads, smem, p.stream>>>(p, m);
     }
     }
     return cudaGetLastError();
@@ -997,7 +1090,7 @@ size_t gn_backward_scratch_bytes(const GroupNorm &p)
     if (p.N == 0) return 0;
     const int vec = p.dtype == DP_F32 ? 4 : 8;
     switch (form_of(p, true)) {
-    case kFormRows: return (size_t)row_ctas(p, row_map(p, vec), 4) * 2 * p.C * sizeof(float);
+    case kFormRows: return (size_t)row_ctas(p, row_map(p, vec, 1), 4) * 2 * p.C * sizeof(float);
     case kFormPositions:
         return (position_part_values(p, position_map(p, vec)) + 2 * (size_t)p.N * p.G) * sizeof(float);
     default: return (size_t)channel_slices(p) * 2 * p.C * sizeof(float);
@@ -1006,12 +1099,16 @@ size_t gn_backward_scratch_bytes(const GroupNorm &p)
 
 cudaError_t launch_gn_forward(const GroupNorm &p)
 {
-    return p.dtype == DP_F32 ? forward_typed<float>(p) : forward_typed<__nv_bfloat16>(p);
+    if (p.act == DP_ACT_SILU)
+        return p.dtype == DP_F32 ? forward_typed<float, DP_ACT_SILU>(p) : forward_typed<__nv_bfloat16, DP_ACT_SILU>(p);
+    return p.dtype == DP_F32 ? forward_typed<float, DP_ACT_NONE>(p) : forward_typed<__nv_bfloat16, DP_ACT_NONE>(p);
 }
 
 cudaError_t launch_gn_backward(const GroupNorm &p)
 {
-    return p.dtype == DP_F32 ? backward_typed<float>(p) : backward_typed<__nv_bfloat16>(p);
+    if (p.act == DP_ACT_SILU)
+        return p.dtype == DP_F32 ? backward_typed<float, DP_ACT_SILU>(p) : backward_typed<__nv_bfloat16, DP_ACT_SILU>(p);
+    return p.dtype == DP_F32 ? backward_typed<float, DP_ACT_NONE>(p) : backward_typed<__nv_bfloat16, DP_ACT_NONE>(p);
 }
 
 }  // namespace dp

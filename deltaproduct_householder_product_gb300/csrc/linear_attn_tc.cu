@@ -37,6 +37,7 @@
 // follow, la_tc_kernel then starts every segment from the decayed sum of the
 // states before it (two launches; rows that stay in L2 are read from there
 // the second time).
+#include "f32x2.cuh"
 #include "linear_attn.h"
 #include "sm100.cuh"
 #include "tensor_map.h"
@@ -249,29 +250,6 @@ __device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t (&r)
     asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
                  "r"(r[2]), "r"(r[3])
                  : "memory");
-}
-// two fp32 at once
-__device__ __forceinline__ uint64_t pair(float a, float b)
-{
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-    return d;
-}
-__device__ __forceinline__ void unpair(uint64_t d, float &a, float &b)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
 }
 // two bf16 at once
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
