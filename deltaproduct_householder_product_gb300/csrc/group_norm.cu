@@ -122,6 +122,24 @@ template <typename T, int ACT> __device__ __forceinline__ uint64_t act_grad2(uin
     return mul2(p, fma2(z, fma2(p, pair(-1.f, -1.f), one), one));
 }
 
+// one piece as it lies in memory, and as fp32
+template <typename T, int K> struct Raw {
+    uint4 v;
+    __device__ __forceinline__ void load(const T *p) { v = *(const uint4 *)p; }
+    __device__ __forceinline__ void get(float (&f)[K]) const
+    {
+        uint64_t x[K / 2];
+        widen<T>(v, x);
+#pragma unroll
+        for (int k = 0; k < K / 2; ++k) unpair(x[k], f[2 * k], f[2 * k + 1]);
+    }
+};
+template <typename T> struct Raw<T, 1> {
+    T v;
+    __device__ __forceinline__ void load(const T *p) { v = *p; }
+    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = ld(&v, 0); }
+};
+
 // sum over the `lanes` (a power of two) neighbouring lanes of a group
 __device__ __forceinline__ float lane_sum(float v, int lanes)
 {
@@ -642,7 +660,11 @@ struct PositionMap {
     int slices, per;        // slices of a sample; rows of a slice
 };
 
-PositionMap position_map(const GroupNorm &p, int vec)
+constexpr int kAhead = 4;       // rows whose loads a thread has in flight
+// CTAs wanted for each SM: as many as its registers hold at once
+constexpr int kPerSmForward = 4, kPerSmGrad = 2;
+
+PositionMap position_map(const GroupNorm &p, int vec, int per_sm)
 {
     PositionMap m;
     m.K = p.C % vec == 0 ? vec : 1;
@@ -650,8 +672,8 @@ PositionMap position_map(const GroupNorm &p, int vec)
     m.cols = pieces < kThreads ? pieces : kThreads;
     m.rows = kThreads / m.cols;
     m.blocks = (pieces + m.cols - 1) / m.cols;
-    // about four CTAs for each of the SMs, and at least four turns for each
-    const long long want = (4 * 152 + p.N * m.blocks - 1) / (p.N * m.blocks);
+    // enough CTAs for the SMs, and at least four turns for each
+    const long long want = (per_sm * 152 + p.N * m.blocks - 1) / (p.N * m.blocks);
     const long long most = (p.S + 4 * m.rows - 1) / (4 * m.rows);
     m.slices = (int)(want < most ? want : most);
     if (m.slices < 1) m.slices = 1;
@@ -804,14 +826,21 @@ gn_position_apply_kernel(GroupNorm p, PositionMap m, const float *mean, const fl
     ch.load(p, mean, rstd, n, piece * K);
     const int s0 = slice * m.per, s1 = s0 + m.per < p.S ? s0 + m.per : p.S;
     const size_t at = (size_t)n * p.S * p.C + (size_t)piece * K;
-#pragma unroll 4
-    for (int s = s0 + row; s < s1; s += m.rows) {
-        float f[K];
-        Piece<T, K>::load((const T *)p.x + at + (size_t)s * p.C, f);
+    for (int s = s0 + row; s < s1; s += kAhead * m.rows) {
+        Raw<T, K> rx[kAhead];
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            f[k] = act_fwd<T, ACT>(fmaf((f[k] - ch.mean[k]) * ch.rstd[k], ch.w[k], ch.b[k]));
-        Piece<T, K>::store((T *)p.y + at + (size_t)s * p.C, f);
+        for (int i = 0; i < kAhead; ++i)
+            if (s + i * m.rows < s1) rx[i].load((const T *)p.x + at + (size_t)(s + i * m.rows) * p.C);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (s + i * m.rows < s1) {
+                float f[K];
+                rx[i].get(f);
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    f[k] = act_fwd<T, ACT>(fmaf((f[k] - ch.mean[k]) * ch.rstd[k], ch.w[k], ch.b[k]));
+                Piece<T, K>::store((T *)p.y + at + (size_t)(s + i * m.rows) * p.C, f);
+            }
     }
 }
 
@@ -836,17 +865,27 @@ gn_position_grad_kernel(GroupNorm p, PositionMap m, float *part)
         float a[K], q[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) a[k] = q[k] = 0.f;
-#pragma unroll 2
-        for (int s = s0 + row; s < s1; s += m.rows) {
-            float x[K], d[K];
-            Piece<T, K>::load((const T *)p.x + at + (size_t)s * p.C, x);
-            Piece<T, K>::load((const T *)p.dy + at + (size_t)s * p.C, d);
-            grads<T, K, ACT>(x, d, ch.mean, ch.rstd, ch.w, ch.b);
+        for (int s = s0 + row; s < s1; s += kAhead * m.rows) {
+            Raw<T, K> rx[kAhead], rd[kAhead];
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                a[k] = fmaf(d[k], x[k], a[k]);
-                q[k] += d[k];
-            }
+            for (int i = 0; i < kAhead; ++i)
+                if (s + i * m.rows < s1) {
+                    rx[i].load((const T *)p.x + at + (size_t)(s + i * m.rows) * p.C);
+                    rd[i].load((const T *)p.dy + at + (size_t)(s + i * m.rows) * p.C);
+                }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (s + i * m.rows < s1) {
+                    float x[K], d[K];
+                    rx[i].get(x);
+                    rd[i].get(d);
+                    grads<T, K, ACT>(x, d, ch.mean, ch.rstd, ch.w, ch.b);
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        a[k] = fmaf(d[k], x[k], a[k]);
+                        q[k] += d[k];
+                    }
+                }
         }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -910,15 +949,25 @@ gn_position_dx_kernel(GroupNorm p, PositionMap m, const float2 *sums)
     }
     const int s0 = slice * m.per, s1 = s0 + m.per < p.S ? s0 + m.per : p.S;
     const size_t at = (size_t)n * p.S * p.C + (size_t)piece * K;
-#pragma unroll 2
-    for (int s = s0 + row; s < s1; s += m.rows) {
-        float x[K], d[K];
-        Piece<T, K>::load((const T *)p.x + at + (size_t)s * p.C, x);
-        Piece<T, K>::load((const T *)p.dy + at + (size_t)s * p.C, d);
-        grads<T, K, ACT>(x, d, ch.mean, ch.rstd, ch.w, ch.b);
+    for (int s = s0 + row; s < s1; s += kAhead * m.rows) {
+        Raw<T, K> rx[kAhead], rd[kAhead];
 #pragma unroll
-        for (int k = 0; k < K; ++k) d[k] = ch.rstd[k] * (fmaf(d[k], ch.w[k], -mu[k]) - x[k] * muh[k]);
-        Piece<T, K>::store((T *)p.dx + at + (size_t)s * p.C, d);
+        for (int i = 0; i < kAhead; ++i)
+            if (s + i * m.rows < s1) {
+                rx[i].load((const T *)p.x + at + (size_t)(s + i * m.rows) * p.C);
+                rd[i].load((const T *)p.dy + at + (size_t)(s + i * m.rows) * p.C);
+            }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (s + i * m.rows < s1) {
+                float x[K], d[K];
+                rx[i].get(x);
+                rd[i].get(d);
+                grads<T, K, ACT>(x, d, ch.mean, ch.rstd, ch.w, ch.b);
+#pragma unroll
+                for (int k = 0; k < K; ++k) d[k] = ch.rstd[k] * (fmaf(d[k], ch.w[k], -mu[k]) - x[k] * muh[k]);
+                Piece<T, K>::store((T *)p.dx + at + (size_t)(s + i * m.rows) * p.C, d);
+            }
     }
 }
 
@@ -1025,7 +1074,7 @@ cudaError_t forward_typed(const GroupNorm &p)
         break;
     }
     case kFormPositions: {
-        const PositionMap m = position_map(p, K);
+        const PositionMap m = position_map(p, K, kPerSmForward);
         return m.K == K ? forward_positions<T, K, ACT>(p, m) : forward_positions<T, 1, ACT>(p, m);
     }
     default: gn_wide_kernel<T, ACT><<<(unsigned)(p.N * p.G), kThreads, 0, p.stream>>>(p);
@@ -1050,7 +1099,7 @@ cudaError_t backward_typed(const GroupNorm &p)
         break;
     }
     case kFormPositions: {
-        const PositionMap m = position_map(p, K);
+        const PositionMap m = position_map(p, K, kPerSmGrad);
         return m.K == K ? backward_positions<T, K, ACT>(p, m) : backward_positions<T, 1, ACT>(p, m);
     }
     default: {
@@ -1081,7 +1130,7 @@ cudaError_t backward_typed(const GroupNorm &p)
 size_t gn_forward_scratch_bytes(const GroupNorm &p)
 {
     if (p.N == 0 || form_of(p, false) != kFormPositions) return 0;
-    const PositionMap m = position_map(p, p.dtype == DP_F32 ? 4 : 8);
+    const PositionMap m = position_map(p, p.dtype == DP_F32 ? 4 : 8, kPerSmForward);
     return (position_part_values(p, m) + 2 * (size_t)p.N * p.G) * sizeof(float);
 }
 
@@ -1092,7 +1141,7 @@ size_t gn_backward_scratch_bytes(const GroupNorm &p)
     switch (form_of(p, true)) {
     case kFormRows: return (size_t)row_ctas(p, row_map(p, vec, 1), 4) * 2 * p.C * sizeof(float);
     case kFormPositions:
-        return (position_part_values(p, position_map(p, vec)) + 2 * (size_t)p.N * p.G) * sizeof(float);
+        return (position_part_values(p, position_map(p, vec, kPerSmGrad)) + 2 * (size_t)p.N * p.G) * sizeof(float);
     default: return (size_t)channel_slices(p) * 2 * p.C * sizeof(float);
     }
 }
