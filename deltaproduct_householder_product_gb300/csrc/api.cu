@@ -499,7 +499,7 @@ dp_status check_la_dims(const dp_la_dims *d, bool step, bool varlen)
     // rows are counted in int, a segment's end past the last one included;
     // the grid is one CTA per sequence, head and segment
     if (!step && d->T > (1 << 30)) return DP_ERR_UNSUPPORTED;
-    if ((long long)d->B * d->H * dp::kLaMaxSegments > 0x7fffffffll) return DP_ERR_UNSUPPORTED;
+    if ((long long)d->B * d->H * dp::kLaMaxSegments * 3 > 0x7fffffffll) return DP_ERR_UNSUPPORTED;
     if (d->impl == DP_IMPL_CHUNK_TC && !dp::la_tc_supported(d->dtype)) return DP_ERR_UNSUPPORTED;
     return DP_OK;
 }
@@ -507,7 +507,7 @@ dp_status check_la_dims(const dp_la_dims *d, bool step, bool varlen)
 bool la_tc(const dp_la_dims *d) { return d->impl != DP_IMPL_RECURRENT && dp::la_tc_supported(d->dtype); }
 bool la_varlen(const dp_la_dims *d) { return d && d->max_seqlen != 0; }
 
-int la_segments(const dp_la_dims *d)
+int la_segments(const dp_la_dims *d, bool grad)
 {
     const int longest = d->max_seqlen > 0 ? d->max_seqlen : d->T;
     if (!la_tc(d)) return dp::la_simt_cluster(d->B, d->H, longest);
@@ -517,18 +517,19 @@ int la_segments(const dp_la_dims *d)
         cudaGetLastError();
         return 1;   // no device: one segment, which every device can run
     }
-    return dp::la_tc_segments(d->B, d->H, d->T, longest, d->max_seqlen > 0, sms);
+    return dp::la_tc_segments(d->B, d->H, d->T, longest, d->max_seqlen > 0, grad ? 3 : 1, sms);
 }
 
-cudaError_t la_launch(const dp_la_dims *d, const dp::LaPass &p)
+// bytes of one pass's segment states; the tensor-core gradients run their
+// three passes at once
+size_t la_part_bytes(const dp_la_dims *d, int P)
 {
-    return la_tc(d) ? dp::launch_la_tc(p) : dp::launch_la_simt(p);
+    return P > 1 ? (size_t)d->B * d->H * P * dp::la_part_cells(d->Dk, d->Dv) * sizeof(float) : 0;
 }
 
-size_t la_workspace(const dp_la_dims *d)
+size_t la_workspace(const dp_la_dims *d, bool grad)
 {
-    const int P = la_segments(d);
-    return kStatusBlock + (P > 1 ? (size_t)d->B * d->H * P * dp::la_part_cells(d->Dk, d->Dv) * sizeof(float) : 0);
+    return kStatusBlock + la_part_bytes(d, la_segments(d, grad)) * (grad && la_tc(d) ? 3 : 1);
 }
 
 dp_status check_workspace(const void *workspace, size_t bytes, size_t need)
@@ -538,7 +539,8 @@ dp_status check_workspace(const void *workspace, size_t bytes, size_t need)
     return device_pointer(workspace) ? DP_OK : DP_ERR_INVALID_ARG;
 }
 
-dp::LaPass la_pass(const dp_la_dims *d, const int *cu, const float *log_decay, void *workspace, dp_stream_t stream)
+dp::LaPass la_pass(const dp_la_dims *d, bool grad, const int *cu, const float *log_decay, void *workspace,
+                   dp_stream_t stream)
 {
     dp::LaPass p;
     memset(&p, 0, sizeof(p));
@@ -547,7 +549,7 @@ dp::LaPass la_pass(const dp_la_dims *d, const int *cu, const float *log_decay, v
     p.log_decay = log_decay;
     p.cu = cu;
     p.max_T = d->max_seqlen > 0 ? d->max_seqlen : d->T;
-    p.P = la_segments(d);
+    p.P = la_segments(d, grad);
     p.status = (uint32_t *)workspace;
     p.part = (float *)((char *)workspace + kStatusBlock);
     p.stream = (cudaStream_t)stream;
@@ -565,11 +567,11 @@ dp_status la_forward(const dp_la_dims *dims, const int *cu, const void *q, const
     if (cu) DP_TRY(check_ptr(cu, 4));
     if (h0) DP_TRY(check_ptr(h0, 16));
     if (h_final) DP_TRY(check_ptr(h_final, 16));
-    DP_TRY(check_workspace(workspace, workspace_bytes, la_workspace(dims)));
-    dp::LaPass p = la_pass(dims, cu, log_decay, workspace, stream);
+    DP_TRY(check_workspace(workspace, workspace_bytes, la_workspace(dims, false)));
+    dp::LaPass p = la_pass(dims, false, cu, log_decay, workspace, stream);
     p.x = q; p.y = k; p.z = v; p.out = o;
     p.init = h0; p.fin = h_final;
-    return from_cuda(la_launch(dims, p));
+    return from_cuda(la_tc(dims) ? dp::launch_la_tc(p) : dp::launch_la_simt(p));
 }
 
 dp_status la_backward(const dp_la_dims *dims, const int *cu, const void *q, const void *k, const void *v,
@@ -585,21 +587,32 @@ dp_status la_backward(const dp_la_dims *dims, const int *cu, const void *q, cons
     if (h0) DP_TRY(check_ptr(h0, 16));
     if (dh_final) DP_TRY(check_ptr(dh_final, 16));
     if (dh0) DP_TRY(check_ptr(dh0, 16));
-    DP_TRY(check_workspace(workspace, workspace_bytes, la_workspace(dims)));
-    const dp::LaPass base = la_pass(dims, cu, log_decay, workspace, stream);
-    dp::LaPass p = base;                      // dq_t = S_t d_o_t
-    p.Dx = dims->Dv; p.Dz = dims->Dk;
-    p.x = d_o; p.y = v; p.z = k; p.out = dq;
-    p.init = h0; p.state_t = true;
-    cudaError_t e = la_launch(dims, p);
-    if (e != cudaSuccess) return from_cuda(e);
-    p.x = v; p.y = d_o; p.z = q; p.out = dk;  // dk_t = G_t v_t
-    p.init = dh_final; p.reverse = true;
-    if ((e = la_launch(dims, p)) != cudaSuccess) return from_cuda(e);
-    p = base;                                 // dv_t = G_t^T k_t, and the only pass that writes dh0
-    p.x = k; p.y = q; p.z = d_o; p.out = dv;
-    p.init = dh_final; p.fin = dh0; p.reverse = true;
-    return from_cuda(la_launch(dims, p));
+    DP_TRY(check_workspace(workspace, workspace_bytes, la_workspace(dims, true)));
+    const dp::LaPass base = la_pass(dims, true, cu, log_decay, workspace, stream);
+    dp::LaPass p[3] = {base, base, base};
+    p[0].Dx = p[1].Dx = dims->Dv;
+    p[0].Dz = p[1].Dz = dims->Dk;
+    p[0].state_t = p[1].state_t = true;
+    p[1].reverse = p[2].reverse = true;
+    p[0].x = d_o; p[0].y = v; p[0].z = k; p[0].out = dq; p[0].init = h0;           // dq_t = S_t d_o_t
+    p[1].x = v; p[1].y = d_o; p[1].z = q; p[1].out = dk; p[1].init = dh_final;     // dk_t = G_t v_t
+    p[2].x = k; p[2].y = q; p[2].z = d_o; p[2].out = dv; p[2].init = dh_final;     // dv_t = G_t^T k_t
+    p[2].fin = dh0;
+    if (la_tc(dims)) {
+        const size_t part = la_part_bytes(dims, base.P) / sizeof(float);
+        p[1].part += part;
+        p[2].part += 2 * part;
+        // dh0 over dh_final: dk has to have read it first
+        const uintptr_t a = (uintptr_t)dh0, b = (uintptr_t)dh_final;
+        const size_t bytes = (size_t)dims->B * dims->H * dims->Dk * dims->Dv * sizeof(float);
+        const bool apart = dh0 && dh_final && (a < b ? b - a : a - b) < bytes;
+        return from_cuda(dp::launch_la_grad_tc(p, apart));
+    }
+    for (const dp::LaPass &pass : p) {   // dv, which writes dh0, comes last
+        const cudaError_t e = dp::launch_la_simt(pass);
+        if (e != cudaSuccess) return from_cuda(e);
+    }
+    return DP_OK;
 }
 
 }  // namespace
@@ -610,13 +623,16 @@ dp_status dp_linear_attention_workspace_size(const dp_la_dims *dims, size_t *byt
 {
     if (!bytes) return DP_ERR_INVALID_ARG;
     DP_TRY(check_la_dims(dims, false, la_varlen(dims)));
-    *bytes = la_workspace(dims);
+    *bytes = la_workspace(dims, false);
     return DP_OK;
 }
 
 dp_status dp_linear_attention_backward_workspace_size(const dp_la_dims *dims, size_t *bytes)
 {
-    return dp_linear_attention_workspace_size(dims, bytes);
+    if (!bytes) return DP_ERR_INVALID_ARG;
+    DP_TRY(check_la_dims(dims, false, la_varlen(dims)));
+    *bytes = la_workspace(dims, true);
+    return DP_OK;
 }
 
 dp_status dp_linear_attention(const dp_la_dims *dims, const void *q, const void *k, const void *v,

@@ -58,8 +58,11 @@ cudaError_t launch_la_simt(const LaPass &p);
 
 // Tensor-core kernel: bf16, any supported size.
 bool la_tc_supported(int dtype);
-int la_tc_segments(int N, int H, int T, int max_T, bool packed, int sms);
+int la_tc_segments(int N, int H, int T, int max_T, bool packed, int passes, int sms);
 cudaError_t launch_la_tc(const LaPass &p);
+// The gradients: the passes of dq, dk and dv, each with its own `part`.
+// `apart`: dv's final state may lie over dk's initial one, so dv runs after.
+cudaError_t launch_la_grad_tc(const LaPass (&p)[3], bool apart);
 
 // One token: state <- gamma state + k v^T, o = state^T q.
 struct LaStep {

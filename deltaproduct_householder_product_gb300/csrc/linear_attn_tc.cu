@@ -65,6 +65,31 @@ struct Params {
     int state_t;
 };
 
+// The gradients' three passes in one launch, dq (0), dk (1) and dv (2): the two
+// that run in reverse read the same rows at the same time, from neighbouring
+// CTAs. A launch may take some of them only: reverse passes first_rev ..
+// first_rev + n_rev - 1, and dq after them.
+struct GradMaps {
+    CUtensorMap q, k, v, d, dq, dk, dv;
+};
+struct GradParams {
+    Params p[3];
+    __nv_bfloat16 *out[3];
+    int first_rev, n_rev;
+
+    // which pass a CTA runs, and which of its segments (`segments` a head)
+    __device__ __forceinline__ int pass_of(unsigned block, int segments, unsigned *job) const
+    {
+        const unsigned reverse = (unsigned)p[0].N * p[0].H * segments * n_rev;
+        if (block >= reverse) {
+            *job = block - reverse;
+            return 0;
+        }
+        *job = block / n_rev;
+        return first_rev + (int)(block - *job * n_rev);
+    }
+};
+
 // What both kernels' roles share: one segment of one (sequence, head).
 struct Cta {
     uint8_t *base;
@@ -694,16 +719,15 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
     e.store_part(c.g.rank);
 }
 
-// One CTA per segment that another one follows: its state into the workspace.
+// One CTA per segment that another one follows (`job` counts them): its state
+// into the workspace.
 template <int DXP, int DZP, bool REV>
-__global__ void __launch_bounds__(kThreads, 1)
-la_state_kernel(const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz, const Params p)
+__device__ __forceinline__ void body(uint8_t *smem, const CUtensorMap *my, const CUtensorMap *mz, const Params &p,
+                                     unsigned job)
 {
     using L = Layout<DXP, DZP>;
-    extern __shared__ __align__(1024) uint8_t smem[];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     Cta c;
-    const unsigned head = blockIdx.x / (p.P - 1), rank = blockIdx.x - head * (p.P - 1) + (REV ? 1 : 0);
+    const unsigned head = job / (p.P - 1), rank = job - head * (p.P - 1) + (REV ? 1 : 0);
     c.g = la_segment(p.cu, p.N, p.T, p.H, p.max_T, p.P, kC, head * p.P + rank);
     if (!c.g.ok) return;    // reported by the kernel that follows
     uint32_t *slot = setup<REV>(c, p, smem);
@@ -724,12 +748,41 @@ la_state_kernel(const __grid_constant__ CUtensorMap my, const __grid_constant__ 
     c.tmem = *slot;
     if (warp < kStateWarps) seg::state_role<DXP, DZP, REV>(c, p);
     else if (warp == kMmaWarp) seg::mma_role<DXP, DZP, REV>(c);
-    else if (lane == 0) seg::load_role<DXP, DZP, REV>(c, &my, &mz);
+    else if (lane == 0) seg::load_role<DXP, DZP, REV>(c, my, mz);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *c.abort && c.status) atomicCAS(c.status, 0u, (uint32_t)kDevTimeout);
     if (warp == kMmaWarp) tmem_dealloc(c.tmem, kTmemCols);
+}
+
+template <int DXP, int DZP, bool REV>
+__global__ void __launch_bounds__(kThreads, 1)
+la_state_kernel(const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz, const Params p)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    body<DXP, DZP, REV>(smem, &my, &mz, p, blockIdx.x);
+}
+
+template <int DKP, int DVP>
+__global__ void __launch_bounds__(kThreads, 1)
+la_grad_state_kernel(const __grid_constant__ GradMaps m, const __grid_constant__ GradParams g)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    unsigned job;
+    const int pass = g.pass_of(blockIdx.x, g.p[0].P - 1, &job);
+    if (pass == 0) {
+        body<DVP, DKP, false>(smem, &m.v, &m.k, g.p[0], job);
+    } else if (DKP == DVP) {   // one body for both: less code at work at once
+        const bool k = pass == 1;
+        body<DKP, DVP, true>(smem, k ? &m.d : &m.q, k ? &m.q : &m.d, g.p[pass], job);
+    } else if (pass == 1) {
+        body<DVP, DKP, true>(smem, &m.d, &m.q, g.p[1], job);
+    } else {
+        body<DKP, DVP, true>(smem, &m.q, &m.d, g.p[2], job);
+    }
 }
 
 }  // namespace seg
@@ -1113,15 +1166,12 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
 }
 
 template <int DXP, int DZP, bool REV>
-__global__ void __launch_bounds__(kThreads, 1)
-la_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
-             const __grid_constant__ CUtensorMap mz, const __grid_constant__ CUtensorMap mo, const Params p,
-             __nv_bfloat16 *out)
+__device__ __forceinline__ void body(uint8_t *smem, const CUtensorMap *mx, const CUtensorMap *my,
+                                     const CUtensorMap *mz, const CUtensorMap *mo, const Params &p,
+                                     __nv_bfloat16 *out, unsigned job)
 {
-    using L = Layout<DXP, DZP>;
-    extern __shared__ __align__(1024) uint8_t smem[];
     Cta c;
-    c.g = la_segment(p.cu, p.N, p.T, p.H, p.max_T, p.P, kC, blockIdx.x);
+    c.g = la_segment(p.cu, p.N, p.T, p.H, p.max_T, p.P, kC, job);
     if (!c.g.ok) {
         if (threadIdx.x == 0 && c.g.h == 0 && c.g.rank == 0) report_bad_sequence(p.status);
         asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1160,14 +1210,44 @@ la_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
     } else if (warp == kStateMmaWarp) {
         state_mma_role<DXP, DZP, REV>(c);
     } else if (lane == 0) {
-        if (warp == kLoadWarp) load_role<DXP, DZP, REV>(c, &mx, &my, &mz);
-        else store_role<DXP, DZP, REV>(c, &mo);
+        if (warp == kLoadWarp) load_role<DXP, DZP, REV>(c, mx, my, mz);
+        else store_role<DXP, DZP, REV>(c, mo);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *c.abort && c.status) atomicCAS(c.status, 0u, (uint32_t)kDevTimeout);
     if (warp == kStateMmaWarp) tmem_dealloc(c.tmem, kTmemCols);
+}
+
+template <int DXP, int DZP, bool REV>
+__global__ void __launch_bounds__(kThreads, 1)
+la_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
+             const __grid_constant__ CUtensorMap mz, const __grid_constant__ CUtensorMap mo, const Params p,
+             __nv_bfloat16 *out)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    body<DXP, DZP, REV>(smem, &mx, &my, &mz, &mo, p, out, blockIdx.x);
+}
+
+template <int DKP, int DVP>
+__global__ void __launch_bounds__(kThreads, 1)
+la_grad_kernel(const __grid_constant__ GradMaps m, const __grid_constant__ GradParams g)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    unsigned job;
+    const int pass = g.pass_of(blockIdx.x, g.p[0].P, &job);
+    if (pass == 0) {
+        body<DVP, DKP, false>(smem, &m.d, &m.v, &m.k, &m.dq, g.p[0], g.out[0], job);
+    } else if (DKP == DVP) {
+        const bool k = pass == 1;
+        body<DKP, DVP, true>(smem, k ? &m.v : &m.k, k ? &m.d : &m.q, k ? &m.q : &m.d, k ? &m.dk : &m.dv, g.p[pass],
+                             g.out[pass], job);
+    } else if (pass == 1) {
+        body<DVP, DKP, true>(smem, &m.v, &m.d, &m.q, &m.dk, g.p[1], g.out[1], job);
+    } else {
+        body<DKP, DVP, true>(smem, &m.k, &m.q, &m.d, &m.dv, g.p[2], g.out[2], job);
+    }
 }
 
 bool rows_map(CUtensorMap *map, const void *base, int D, const LaPass &p)
@@ -1179,64 +1259,102 @@ bool rows_map(CUtensorMap *map, const void *base, int D, const LaPass &p)
     return encode(map, base, 4, dims, strides, box);
 }
 
-template <int DXP, int DZP, bool REV>
-cudaError_t launch_sized(const LaPass &p, const CUtensorMap (&m)[4])
+Params params_of(const LaPass &p)
 {
-    const Params pr{p.N, p.T, p.H, p.Dx, p.Dz, p.max_T, p.P, p.log_decay, p.init, p.fin, p.part, p.cu, p.status,
-                    p.state_t ? 1 : 0};
-    cudaError_t e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.stream = p.stream;
-    if (p.P > 1) {
-        auto states = seg::la_state_kernel<DXP, DZP, REV>;
-        cfg.gridDim = dim3((unsigned)((size_t)p.N * p.H * (p.P - 1)));
-        cfg.blockDim = dim3(seg::kThreads);
-        cfg.dynamicSmemBytes = seg::Layout<DXP, DZP>::bytes;
-        e = cudaFuncSetAttribute(states, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
-        if (e != cudaSuccess) return e;
-        if ((e = cudaLaunchKernelEx(&cfg, states, m[1], m[2], pr)) != cudaSuccess) return e;
-    }
-    auto kernel = la_tc_kernel<DXP, DZP, REV>;
-    cfg.gridDim = dim3((unsigned)((size_t)p.N * p.H * p.P));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Layout<DXP, DZP>::bytes;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    return Params{p.N, p.T, p.H, p.Dx, p.Dz, p.max_T, p.P, p.log_decay, p.init, p.fin, p.part, p.cu, p.status,
+                  p.state_t ? 1 : 0};
+}
+
+// `after`: the kernel's CTAs may start, and load their first rows, while the
+// launch before it (the segments' states) finishes
+template <typename... A, typename... B>
+cudaError_t launch(void (*kernel)(A...), size_t grid, int threads, uint32_t smem, bool after, cudaStream_t stream,
+                   const B &...args)
+{
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    // its CTAs may start, and load their first rows, while the last of the
-    // segments' states are being made
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = p.P > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], pr, (__nv_bfloat16 *)p.out);
+    cfg.numAttrs = after ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int DXP, int DZP>
-cudaError_t launch_dir(const LaPass &p, const CUtensorMap (&m)[4])
+cudaError_t launch_forward(const LaPass &p, const CUtensorMap (&m)[4])
 {
-    return p.reverse ? launch_sized<DXP, DZP, true>(p, m) : launch_sized<DXP, DZP, false>(p, m);
+    const Params pr = params_of(p);
+    const size_t heads = (size_t)p.N * p.H;
+    if (p.P > 1) {
+        const cudaError_t e = launch(seg::la_state_kernel<DXP, DZP, false>, heads * (p.P - 1), seg::kThreads,
+                                     seg::Layout<DXP, DZP>::bytes, false, p.stream, m[1], m[2], pr);
+        if (e != cudaSuccess) return e;
+    }
+    return launch(la_tc_kernel<DXP, DZP, false>, heads * p.P, kThreads, Layout<DXP, DZP>::bytes, p.P > 1, p.stream,
+                  m[0], m[1], m[2], m[3], pr, (__nv_bfloat16 *)p.out);
+}
+
+template <int DKP, int DVP>
+cudaError_t launch_passes(const LaPass (&p)[3], const GradMaps &m, int first_rev, int n_rev, bool with_dq)
+{
+    GradParams g;
+    for (int i = 0; i < 3; ++i) {
+        g.p[i] = params_of(p[i]);
+        g.out[i] = (__nv_bfloat16 *)p[i].out;
+    }
+    g.first_rev = first_rev;
+    g.n_rev = n_rev;
+    const size_t heads = (size_t)p[0].N * p[0].H, passes = n_rev + (with_dq ? 1 : 0);
+    const int P = p[0].P;
+    constexpr uint32_t a = seg::Layout<DKP, DVP>::bytes, b = seg::Layout<DVP, DKP>::bytes;
+    constexpr uint32_t c = Layout<DKP, DVP>::bytes, d = Layout<DVP, DKP>::bytes;
+    if (P > 1) {
+        const cudaError_t e = launch(seg::la_grad_state_kernel<DKP, DVP>, heads * (P - 1) * passes, seg::kThreads,
+                                     a > b ? a : b, false, p[0].stream, m, g);
+        if (e != cudaSuccess) return e;
+    }
+    return launch(la_grad_kernel<DKP, DVP>, heads * P * passes, kThreads, c > d ? c : d, P > 1, p[0].stream, m, g);
+}
+
+template <int DKP, int DVP>
+cudaError_t launch_grad(const LaPass (&p)[3], const GradMaps &m, bool apart)
+{
+    if (!apart) return launch_passes<DKP, DVP>(p, m, 1, 2, true);
+    const cudaError_t e = launch_passes<DKP, DVP>(p, m, 1, 1, true);
+    return e != cudaSuccess ? e : launch_passes<DKP, DVP>(p, m, 2, 1, false);
 }
 
 }  // namespace
 
 bool la_tc_supported(int dtype) { return dtype == DP_BF16 && tensor_map_encoder() != nullptr; }
 
-// The number of segments with the least time, in units of a chunk's outputs:
-// a chunk's state alone costs about half of one, a CTA's start and end about
-// one and a half, the second launch two more. Dense sequences run in waves of
-// one CTA per SM; packed ones are bounded by the mean load plus one segment.
-int la_tc_segments(int N, int H, int T, int max_T, bool packed, int sms)
+// The number of segments with the least time, in units of a chunk's outputs
+// (about 3 us): a chunk's state alone costs about half of one, a CTA's start
+// and end about one and a half, the second launch one more. `passes`: 1, or
+// the gradients' 3. Dense sequences run in waves of one CTA per SM; packed
+// ones, whose lengths the host does not know, are bounded by the mean load
+// plus one segment of the longest.
+int la_tc_segments(int N, int H, int T, int max_T, bool packed, int passes, int sms)
 {
-    const double chunks = (max_T + kC - 1) / kC, heads = (double)N * H;
+    const double chunks = ceil((double)max_T / kC), heads = (double)N * H * passes;
     int best = 1;
     double least = 0;
     for (int P = 1; P <= kLaMaxSegments && (P == 1 || P <= chunks); ++P) {
-        const double seg = ceil(chunks / P) * (P > 1 ? 1.5 : 1.0) + 1.5;
+        const double seg = ceil(chunks / P);
         double t;
-        if (packed) t = ((double)T / kC * H * (P > 1 ? 1.5 : 1.0) + heads * 1.5 * P) / sms + seg;
-        else t = ceil(heads * P / sms) * seg;
-        if (P > 1) t += 2;
+        if (packed) {
+            const double load = (double)T / kC * H * passes / sms;
+            t = (load > seg ? load : seg) * (P > 1 ? 1.5 : 1.0) + (P > 1 ? 3.7 : 3.0) * heads * P / sms;
+        } else {
+            t = ceil(heads * P / sms) * (seg + 1.5);
+            if (P > 1) t += ceil(heads * (P - 1) / sms) * (0.5 * seg + 1.5) + 1;
+        }
         if (P == 1 || t < least) {
             best = P;
             least = t;
@@ -1253,8 +1371,22 @@ cudaError_t launch_la_tc(const LaPass &p)
     if (p.T > 0 && (!rows_map(&m[0], p.x, p.Dx, p) || !rows_map(&m[1], p.y, p.Dx, p) ||
                     !rows_map(&m[2], p.z, p.Dz, p) || !rows_map(&m[3], p.out, p.Dz, p)))
         return cudaErrorInvalidValue;
-    if (p.Dx == 128) return p.Dz == 128 ? launch_dir<128, 128>(p, m) : launch_dir<128, 64>(p, m);
-    return p.Dz == 128 ? launch_dir<64, 128>(p, m) : launch_dir<64, 64>(p, m);
+    if (p.Dx == 128) return p.Dz == 128 ? launch_forward<128, 128>(p, m) : launch_forward<128, 64>(p, m);
+    return p.Dz == 128 ? launch_forward<64, 128>(p, m) : launch_forward<64, 64>(p, m);
+}
+
+cudaError_t launch_la_grad_tc(const LaPass (&p)[3], bool apart)
+{
+    const LaPass &dv = p[2];       // x = k, y = q, z = d_o
+    if ((size_t)dv.N * dv.H == 0) return cudaSuccess;
+    GradMaps m = {};
+    if (dv.T > 0 && (!rows_map(&m.q, dv.y, dv.Dx, dv) || !rows_map(&m.k, dv.x, dv.Dx, dv) ||
+                     !rows_map(&m.v, p[0].y, dv.Dz, dv) || !rows_map(&m.d, dv.z, dv.Dz, dv) ||
+                     !rows_map(&m.dq, p[0].out, dv.Dx, dv) || !rows_map(&m.dk, p[1].out, dv.Dx, dv) ||
+                     !rows_map(&m.dv, dv.out, dv.Dz, dv)))
+        return cudaErrorInvalidValue;
+    if (dv.Dx == 128) return dv.Dz == 128 ? launch_grad<128, 128>(p, m, apart) : launch_grad<128, 64>(p, m, apart);
+    return dv.Dz == 128 ? launch_grad<64, 128>(p, m, apart) : launch_grad<64, 64>(p, m, apart);
 }
 
 }  // namespace dp

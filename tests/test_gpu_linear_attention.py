@@ -358,3 +358,28 @@ def test_refusals(dp):
     host = torch.zeros(1, 2, 64, 64)
     with pytest.raises(ValueError):
         dp.linear_attention(**ok, h0=host)
+
+
+@pytest.mark.parametrize("T,H", [(200, 2), (3000, 1)], ids=str)
+def test_states_over_one_another(dp, T, H):
+    """h_final over h0 and dh0 over dh_final, through the C ABI: the initial
+    value is read in full before the result goes over it, with segments too."""
+    from deltaproduct_householder_product_gb300 import _lib
+    for dtype in (torch.bfloat16, torch.float32):
+        x = draw((1, T, H), 128, 64, dtype, 23, 1)
+        c = {n: t.cuda() for n, t in x.items()}
+        state = c["h0"].clone()
+        o, hf = dp.linear_attention(c["q"], c["k"], c["v"], c["log_decay"], state, h_final=state)
+        check_forward(x, None, o, hf)
+        dims = _lib.make_la_dims(1, T, H, 128, 64, dtype)
+        ws = torch.zeros(dp.linear_attention_workspace_size(1, T, H, 128, 64, dtype=dtype, backward=True),
+                         dtype=torch.uint8, device="cuda")
+        g = {"dq": torch.empty_like(c["q"]), "dk": torch.empty_like(c["k"]), "dv": torch.empty_like(c["v"]),
+             "dh0": c["dh"].clone()}
+        p = _lib._ptr
+        rc = _lib.lib().dp_linear_attention_backward(
+            dims, p(c["q"]), p(c["k"]), p(c["v"]), p(c["log_decay"]), p(c["h0"]), p(c["d_o"]), p(g["dh0"]), p(g["dq"]),
+            p(g["dk"]), p(g["dv"]), p(g["dh0"]), p(ws), ws.numel(), _lib._stream(None))
+        assert rc == 0
+        dp.check_status(ws)
+        check_backward(x, None, g)
