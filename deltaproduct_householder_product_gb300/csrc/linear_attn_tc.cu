@@ -133,6 +133,21 @@ struct Cta {
     {
         return __all_sync(0xffffffffu, wait(b, parity));
     }
+    // The same for a warpgroup: its first warp polls, the others sleep at named
+    // barrier `id`. (Polls of one barrier are served one after another: sixteen
+    // warps at one took some 400 cycles to see it pass.)
+    __device__ __forceinline__ bool wait_group(int id, int b, uint32_t parity) const
+    {
+        int late = 0;
+        if ((threadIdx.x & 127) < 32) late = !wait(b, parity);
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+            "barrier.cta.red.or.aligned.pred q, %1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+            : "=r"(late)
+            : "r"(id), "r"(late)
+            : "memory");
+        return !late;
+    }
     // chunk i in processing order: its first row, live rows
     template <bool REV> __device__ __forceinline__ int row(int i) const
     {
@@ -688,13 +703,13 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
     for (int i = 0; i <= c.chunks; ++i) {
         if (i < c.chunks) {
             const int st = i % kStages, live = c.live<REV>(i);
-            if (!c.wait_warp(bFullY + st, (i / kStages) & 1)) return;
+            if (!c.wait_group(1 + e.group, bFullY + st, (i / kStages) & 1)) return;
             if (c.tail(live)) {
-                if (!c.wait_warp(bFullZ + st, (i / kStages) & 1)) return;
+                if (!c.wait_group(1 + e.group, bFullZ + st, (i / kStages) & 1)) return;
                 e.clear_tail(c.base + st * L::stage + L::off_z, live);
                 arrive_warp(&c.bar[bZReady]);
             }
-            if (i > 0 && !c.wait_warp(bYFree + e.group, (i - 1) & 1)) return;
+            if (i > 0 && !c.wait_group(1 + e.group, bYFree + e.group, (i - 1) & 1)) return;
             tc_fence_after();
             if (e.live_rows) {
                 const uint32_t sy = smem_addr(c.base + st * L::stage);
@@ -709,7 +724,7 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
         }
         if (i > 0) {   // the chunk before, whose MMAs ran meanwhile
             const int b = (i - 1) & 1;
-            if (!c.wait_warp(bBFull + b, ((i - 1) >> 1) & 1)) return;
+            if (!c.wait_group(1 + e.group, bBFull + b, ((i - 1) >> 1) & 1)) return;
             tc_fence_after();
             if (e.live_rows) e.update(c.tmem + kColB + 128 * b, c.live<REV>(i - 1));
             tc_fence_before();
@@ -996,7 +1011,7 @@ __device__ void score_role(const Cta &c)
     const int warp = (threadIdx.x >> 5) - kScoreWarp;
 #pragma unroll 1
     for (int j = 0; j < c.chunks; ++j) {
-        if (!c.wait_warp(bAFull, j & 1)) return;
+        if (!c.wait_group(5, bAFull, j & 1)) return;
         tc_fence_after();
         score_half<REV>(c, warp, 0, c.live<REV>(j));
     }
@@ -1014,12 +1029,12 @@ __device__ void out_role(const Cta &c, __nv_bfloat16 *out, int H, int Dz)
 #pragma unroll 1
     for (int j = 0; j < c.chunks; ++j) {
         const int live = c.live<REV>(j), st = j & 1;
-        if (!c.wait_warp(bAFull, j & 1)) return;
+        if (!c.wait_group(6, bAFull, j & 1)) return;
         tc_fence_after();
         score_half<REV>(c, warp, 1, live);
-        if (!c.wait_warp(bOutFull, j & 1)) return;
+        if (!c.wait_group(6, bOutFull, j & 1)) return;
         tc_fence_after();
-        if (L::own_stage && j > 0 && !c.wait_warp(bStored, (j - 1) & 1)) return;
+        if (L::own_stage && j > 0 && !c.wait_group(6, bStored, (j - 1) & 1)) return;
         uint8_t *tile = c.base + (L::own_stage ? L::off_out : st * L::stage);
 #pragma unroll 1
         for (int b = 0; b < DZP / 32; ++b) {
@@ -1125,7 +1140,7 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
             arrive_warp(&c.bar[bStateReady]);
         }
         if (c.tail(live)) {
-            if (!c.wait_warp(bFullZ + st, (j >> 1) & 1)) return;
+            if (!c.wait_group(1 + e.group, bFullZ + st, (j >> 1) & 1)) return;
             e.clear_tail(c.base + st * L::stage + L::off_z, live);
             arrive_warp(&c.bar[bZReady]);
         }
@@ -1136,8 +1151,8 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
 #pragma unroll 1
         for (; sent < until; ++sent) {
             const int i = sent >> 1, si = i & 1, r0 = 32 * (side + 2 * (sent & 1)) + 16 * (e.group & 1);
-            if (!c.wait_warp(bFullY + si, (i >> 1) & 1)) return;
-            if (sent > 0 && !c.wait_warp(bYFree + side, (sent - 1) & 1)) return;
+            if (!c.wait_group(1 + e.group, bFullY + si, (i >> 1) & 1)) return;
+            if (sent > 0 && !c.wait_group(1 + e.group, bYFree + side, (sent - 1) & 1)) return;
             tc_fence_after();
             if (e.live_rows)
                 e.send_keys(smem_addr(c.base + si * L::stage + L::off_y),
@@ -1148,7 +1163,7 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
             if (sent & 1) arrive_warp(&c.bar[bEmptyY + si]);
         }
         if (c.has0 || j > 0) {
-            if (!c.wait_warp(bInterFull, inter++ & 1)) return;
+            if (!c.wait_group(1 + e.group, bInterFull, inter++ & 1)) return;
             if (!c.mild) {
                 tc_fence_after();
                 e.scale_rows(c.tmem + kColO, live);
@@ -1156,7 +1171,7 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
             }
         }
         if (j >= c.updates) break;
-        if (!c.wait_warp(bBFull, j & 1)) return;
+        if (!c.wait_group(1 + e.group, bBFull, j & 1)) return;
         tc_fence_after();
         if (e.live_rows) e.update(c.tmem + kColB, live);
         tc_fence_before();
