@@ -507,16 +507,22 @@ dp_status check_la_dims(const dp_la_dims *d, bool step, bool varlen)
 bool la_tc(const dp_la_dims *d) { return d->impl != DP_IMPL_RECURRENT && dp::la_tc_supported(d->dtype); }
 bool la_varlen(const dp_la_dims *d) { return d && d->max_seqlen != 0; }
 
+int la_sms()   // 0: no device
+{
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess &&
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+        return sms;
+    cudaGetLastError();
+    return 0;
+}
+
 int la_segments(const dp_la_dims *d, bool grad)
 {
     const int longest = d->max_seqlen > 0 ? d->max_seqlen : d->T;
     if (!la_tc(d)) return dp::la_simt_cluster(d->B, d->H, longest);
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 1;   // no device: one segment, which every device can run
-    }
+    const int sms = la_sms();
+    if (sms == 0) return 1;   // one segment, which every device can run
     return dp::la_tc_segments(d->B, d->H, d->T, longest, d->max_seqlen > 0, grad ? 3 : 1, sms);
 }
 
@@ -527,9 +533,19 @@ size_t la_part_bytes(const dp_la_dims *d, int P)
     return P > 1 ? (size_t)d->B * d->H * P * dp::la_part_cells(d->Dk, d->Dv) * sizeof(float) : 0;
 }
 
+// CTAs that may take a share of the runs where those outnumber the SMs
+int la_shares(const dp_la_dims *d, int P, bool grad)
+{
+    const int sms = la_sms();
+    if (!la_tc(d) || P > 1 || d->max_seqlen > 0 || (long long)d->B * d->H * (grad ? 3 : 1) <= sms) return 0;
+    return sms < dp::kLaMaxShares ? sms : dp::kLaMaxShares;
+}
+
 size_t la_workspace(const dp_la_dims *d, bool grad)
 {
-    return kStatusBlock + la_part_bytes(d, la_segments(d, grad)) * (grad && la_tc(d) ? 3 : 1);
+    const int P = la_segments(d, grad), shares = la_shares(d, P, grad);
+    if (shares > 0) return kStatusBlock + (dp::kLaShareFlags + shares * dp::la_part_cells(d->Dk, d->Dv)) * sizeof(float);
+    return kStatusBlock + la_part_bytes(d, P) * (grad && la_tc(d) ? 3 : 1);
 }
 
 dp_status check_workspace(const void *workspace, size_t bytes, size_t need)
@@ -550,6 +566,7 @@ dp::LaPass la_pass(const dp_la_dims *d, bool grad, const int *cu, const float *l
     p.cu = cu;
     p.max_T = d->max_seqlen > 0 ? d->max_seqlen : d->T;
     p.P = la_segments(d, grad);
+    p.shares = la_shares(d, p.P, grad);
     p.status = (uint32_t *)workspace;
     p.part = (float *)((char *)workspace + kStatusBlock);
     p.stream = (cudaStream_t)stream;

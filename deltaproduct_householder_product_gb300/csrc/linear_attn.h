@@ -37,11 +37,13 @@ struct LaPass {
     int max_T;                 // longest sequence
     int P;                     // segments of a sequence, one CTA each
     float *part;               // states of the segments (P > 1): N H P la_part_cells(..) values
+    int shares;                // P == 1: `part` holds kLaShareFlags words and as many states instead
     uint32_t *status;
     cudaStream_t stream;
 };
 
 constexpr int kLaMaxCluster = 8, kLaMaxSegments = 32;
+constexpr int kLaShareFlags = 1024, kLaMaxShares = kLaShareFlags - 1;
 
 // fp32 values of one segment's state in the workspace (the tensor-core kernel
 // pads the state to 128 rows and at least 64 columns, in either orientation)

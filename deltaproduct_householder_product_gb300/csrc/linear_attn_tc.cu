@@ -53,6 +53,7 @@ constexpr int kC = 128;
 // A wait polls its barrier at most kTries times; each poll may suspend the
 // warp for up to kSuspend ns, so that waiting warps take few issue slots.
 constexpr uint32_t kTries = 1u << 17, kSuspend = 20000;
+constexpr uint32_t kHandTries = 1u << 21;   // of half a microsecond and more
 constexpr uint32_t kSub = 16384;    // one [128 rows][64 columns] bf16 tile, 128-byte swizzle
 constexpr int kStateWarps = 16;     // four warpgroups: a quarter of a chunk's keys, of the state's columns each
 
@@ -90,14 +91,69 @@ struct GradParams {
     }
 };
 
+// Where there are more (sequence, head, pass) runs than SMs, all of one length,
+// whole runs would leave most SMs idle in a last wave. They are laid out on a
+// line instead, chunk after chunk (`width` runs side by side), and the line is
+// cut into equal shares, one CTA each. A share may begin within one run and end
+// within another. A CTA takes its share from the far end: first the run that
+// its share cuts off, whose state goes to the next CTA by a slot, then whole
+// runs, last the rest of the run that the CTA before it began. That one was the
+// other's first, and no run is longer than a share, so its state is there by
+// then but for the CTAs' differences in speed. Shares go by the order in which
+// the CTAs start: each waits only for one that runs already.
+struct Share {
+    uint32_t *flags;              // [0]: CTAs that have started, [1 + i]: warps of CTA i that have handed over
+    float *slots;                 // CTA i's state, at i * cells
+    size_t cells;
+    long long line, per;          // chunks: of the line, of a share (0: a run for each CTA)
+    int chunks;                   // of a run
+    int width;                    // runs side by side
+    unsigned blocks;              // runs in all (the last ones may have fewer neighbours)
+};
+// One CTA's piece of a run: chunks [a, b) in processing order.
+struct Piece {
+    unsigned block;
+    int a, b;
+    int from, to;                 // slots, -1: none
+    int ok;                       // 0: there is none
+};
+__device__ __forceinline__ bool next_piece(const Share &w, unsigned cta, int item, Piece *p)
+{
+    p->from = p->to = -1;
+    const unsigned share = cta / w.width;
+    const long long lo = share * w.per, hi = lo + w.per < w.line ? lo + w.per : w.line;
+    if (lo >= hi) return false;
+    const long long run = (hi - 1) / w.chunks - item, first = run * w.chunks;
+    const long long end = item == 0 ? hi : first + w.chunks;
+    if (end <= lo) return false;
+    p->block = (unsigned)run * w.width + cta % w.width;
+    p->a = lo > first ? (int)(lo - first) : 0;
+    p->b = (int)(end - first);
+    if (p->a > 0) p->from = (int)cta - w.width;
+    if (p->b < w.chunks) p->to = (int)cta;
+    return true;
+}
+
+// Shared memory outside the tiles: barriers, then the tables.
+constexpr uint32_t kAuxBytes = 3072, kAuxTables = 320;
+// at the end of that block: the CTA's place in the order of starts, the TMEM
+// address, the number of its next piece, and the present one
+constexpr uint32_t kAuxTicket = kAuxBytes - 16, kAuxPiece = kAuxTicket - 32;
+// The powers of gamma in the order in which a row of the scores meets them
+// along its columns: gamma^128 .. gamma^0 and then zeros forward, 32 zeros and
+// then gamma^0 .. gamma^128 reverse. A second copy, shifted by one entry, lets
+// a thread read any run of them in aligned pairs; for a mild head its place
+// holds the columns' powers instead, gamma^-(s+1) forward and gamma^-(127-s)
+// reverse.
+constexpr int kPowers = 162;
+constexpr float kMildLog = 0.17328680f;   // 32 ln 2 / 128
+constexpr int kTerms = 4;           // bf16 terms of a weighted key
+
 // What both kernels' roles share: one segment of one (sequence, head).
 struct Cta {
     uint8_t *base;
     uint64_t *bar;
-    uint32_t powers;              // shared: the powers of gamma
-    uint32_t columns;             // shared: a mild head's powers for the scores' columns
-    uint32_t weights;             // shared: the terms of the key weights of a whole chunk, per pair of rows
-    uint32_t pc;                  // shared: gamma^128, gamma^(rows of the ragged chunk), as two fp32 each
+    uint32_t tables;              // shared: the decay's tables
     volatile uint32_t *abort;
     uint32_t *status;
     uint32_t tmem;
@@ -106,6 +162,7 @@ struct Cta {
     int chunks;                   // of this segment
     int updates;                  // of them, those whose rows go into the state
     bool has0;                    // a state enters the segment
+    const volatile Piece *piece;  // shared: what this is of a run
     bool mild;                    // gamma^128 >= 2^-32
     bool packed;
 
@@ -148,6 +205,13 @@ struct Cta {
             : "memory");
         return !late;
     }
+    // the terms of the key weights of a whole chunk, per pair of rows
+    __device__ __forceinline__ uint32_t weights() const { return tables; }
+    // the powers of gamma; a mild head's powers for the scores' columns
+    __device__ __forceinline__ uint32_t powers() const { return tables + 8 * kC; }
+    __device__ __forceinline__ uint32_t columns() const { return powers() + 4 * kPowers; }
+    // gamma^128, gamma^(rows of the ragged chunk), as two fp32 each
+    __device__ __forceinline__ uint32_t pc() const { return columns() + 4 * kPowers; }
     // chunk i in processing order: its first row, live rows
     template <bool REV> __device__ __forceinline__ int row(int i) const
     {
@@ -162,18 +226,6 @@ struct Cta {
     // on into the next sequence
     __device__ __forceinline__ bool tail(int rows) const { return packed && rows < kC; }
 };
-
-// Shared memory outside the tiles: barriers, then the tables.
-constexpr uint32_t kAuxBytes = 3072, kAuxTables = 320;
-// The powers of gamma in the order in which a row of the scores meets them
-// along its columns: gamma^128 .. gamma^0 and then zeros forward, 32 zeros and
-// then gamma^0 .. gamma^128 reverse. A second copy, shifted by one entry, lets
-// a thread read any run of them in aligned pairs; for a mild head its place
-// holds the columns' powers instead, gamma^-(s+1) forward and gamma^-(127-s)
-// reverse.
-constexpr int kPowers = 162;
-constexpr float kMildLog = 0.17328680f;   // 32 ln 2 / 128
-constexpr int kTerms = 4;           // bf16 terms of a weighted key
 
 template <bool REV> __device__ __forceinline__ uint32_t power_at(uint32_t powers, int n)
 {
@@ -201,9 +253,7 @@ __device__ __forceinline__ uint32_t *setup(Cta &c, const Params &p, uint8_t *sme
     float *powers = (float *)(weights + kC / 2);
     float2 *pc = (float2 *)(powers + 2 * kPowers);
     uint32_t *slot = (uint32_t *)(pc + 2);
-    c.weights = smem_addr(weights);
-    c.powers = smem_addr(powers);
-    c.pc = smem_addr(pc);
+    c.tables = smem_addr(weights);
     c.abort = slot + 1;
     c.status = p.status;
     c.packed = p.cu != nullptr;
@@ -211,7 +261,6 @@ __device__ __forceinline__ uint32_t *setup(Cta &c, const Params &p, uint8_t *sme
     c.last_rank = c.g.len > 0 ? (c.g.len - 1) / c.g.seg : 0;
     const float ld = p.log_decay[c.g.h];
     c.mild = fabsf(ld) <= kMildLog;
-    c.columns = smem_addr(powers + kPowers);
     if (threadIdx.x < kPowers) {
         const int n = REV ? (int)threadIdx.x - 32 : 128 - (int)threadIdx.x;
         const float w = n >= 0 && n <= kC ? la_power(ld, n) : 0.f;
@@ -321,8 +370,11 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t &a, ui
                  : "memory");
 }
 
-// Reads of the decay tables, which do not change after the kernel's first
+// Reads of the decay tables, which do not change after a piece's first
 // barrier: not volatile, so that they are issued together ahead of their uses.
+// The tables' address is made opaque at that barrier (fresh_tables), which
+// keeps reads of one piece's tables out of another's.
+__device__ __forceinline__ void fresh_tables(Cta &c) { asm volatile("" : "+r"(c.tables)::"memory"); }
 __device__ __forceinline__ float lds(uint32_t a)
 {
     float f;
@@ -453,16 +505,16 @@ struct State {
     {
         return (float4 *)(p.part + (head * p.P + slot) * (kN * kStateWarps * 32)) + warp * 32 + lane;
     }
-    __device__ __forceinline__ void store_part(int slot) const
+    __device__ __forceinline__ void store_part(int slot) const { put(part(slot)); }
+    __device__ __forceinline__ void add_part(int slot, float w) { add(part(slot), w); }
+    __device__ __forceinline__ void put(float4 *d) const
     {
-        float4 *d = part(slot);
 #pragma unroll
         for (int q = 0; q < kN; q += 4)
             d[(q / 4) * (kStateWarps * 32)] = make_float4(s[q], s[q + 1], s[q + 2], s[q + 3]);
     }
-    __device__ __forceinline__ void add_part(int slot, float w)
+    __device__ __forceinline__ void add(const float4 *d, float w)
     {
-        const float4 *d = part(slot);
         float4 v[kN / 4];
 #pragma unroll
         for (int q = 0; q < kN / 4; ++q) v[q] = __ldcg(d + q * (kStateWarps * 32));
@@ -473,6 +525,37 @@ struct State {
             s[4 * q + 2] = fmaf(w, v[q].z, s[4 * q + 2]);
             s[4 * q + 3] = fmaf(w, v[q].w, s[4 * q + 3]);
         }
+    }
+    // The state of a run that continues in another CTA: warp i's part there is
+    // warp i's here. A wait that runs out is flagged, and the roles end at
+    // their next waits.
+    __device__ __forceinline__ float4 *slot(const Share &w, int i) const
+    {
+        return (float4 *)(w.slots + (size_t)i * w.cells) + warp * 32 + lane;
+    }
+    __device__ __forceinline__ void hand_over(const Share &w) const
+    {
+        put(slot(w, c.piece->to));
+        __threadfence();
+        __syncwarp();
+        if (lane == 0)
+            asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(w.flags + 1 + c.piece->to) : "memory");
+    }
+    __device__ __forceinline__ void take_over(const Share &w)
+    {
+        if (lane == 0) {
+            uint32_t n = 0;
+#pragma unroll 1
+            for (uint32_t i = 0; i < kHandTries && !*c.abort; ++i) {
+                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(w.flags + 1 + c.piece->from) : "memory");
+                if (n == kStateWarps) break;
+                __nanosleep(500);
+            }
+            if (n != kStateWarps) *c.abort = 1;
+        }
+        __syncwarp();
+        __threadfence();
+        add(slot(w, c.piece->from), 1.f);
     }
     __device__ __forceinline__ void clear()
     {
@@ -497,7 +580,7 @@ struct State {
         if (live == kC) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const uint4 w = lds_u4(c.weights + 8 * first + 64 * q);
+                const uint4 w = lds_u4(c.weights() + 8 * first + 64 * q);
                 h[q] = w.x;
                 m[q] = w.y;
                 l[q] = w.z;
@@ -506,8 +589,8 @@ struct State {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int r = first + 8 * q;
-                weight_terms(lds(power_at<REV>(c.powers, REV ? r + 1 : r < live ? live - 1 - r : 0)),
-                             lds(power_at<REV>(c.powers, REV ? r + 2 : r + 1 < live ? live - 2 - r : 0)), h[q], m[q],
+                weight_terms(lds(power_at<REV>(c.powers(), REV ? r + 1 : r < live ? live - 1 - r : 0)),
+                             lds(power_at<REV>(c.powers(), REV ? r + 2 : r + 1 < live ? live - 2 - r : 0)), h[q], m[q],
                              l[q]);
                 // rows past the sequence count as zeros
                 const uint32_t keep = (r < live ? 0xffffu : 0u) | (r + 1 < live ? 0xffff0000u : 0u);
@@ -538,7 +621,7 @@ struct State {
     // E <- gamma^R E + B, B in the TMEM columns at `col`
     __device__ __forceinline__ void update(uint32_t col, int live)
     {
-        const uint32_t pc = c.pc + (live == kC ? 0 : 8);
+        const uint32_t pc = c.pc() + (live == kC ? 0 : 8);
         const float x = lds(pc), y = lds(pc + 4);
         const uint64_t wx = pair(x, x), wy = pair(y, y);
 #pragma unroll
@@ -559,7 +642,7 @@ struct State {
     __device__ __forceinline__ void scale_rows(uint32_t col, int live) const
     {
         const int n = REV ? live - 1 - dx : dx + 1;
-        const float w = n >= 0 ? lds(power_at<REV>(c.powers, n)) : 0.f;
+        const float w = n >= 0 ? lds(power_at<REV>(c.powers(), n)) : 0.f;
         const uint64_t ww = pair(w, w);
         const uint32_t t = col + ((uint32_t)(32 * quarter) << 16) + dz0;
 #pragma unroll
@@ -869,6 +952,8 @@ __device__ void load_role(const Cta &c, const CUtensorMap *mx, const CUtensorMap
 }
 
 // ------------------------------------------------------------------ MMAs of scores and output
+// Nothing is committed to a barrier that no role waits for any more: at the
+// end of a piece every arrival has been seen, and the barriers' memory is free.
 // Descriptors are built once and advanced by an addition to their address field.
 template <int DXP, int DZP, bool REV>
 __device__ void out_mma_role(const Cta &c)
@@ -895,7 +980,7 @@ __device__ void out_mma_role(const Cta &c)
             warp_mma_ss(dA, x + ((k >> 2) * (kSub >> 4) + (k & 3) * 2), y + ((k >> 2) * (kSub >> 4) + (k & 3) * 2),
                         idesc_bf16(kC, kC, false, false), k > 0);
         warp_commit(&c.bar[bAFull]);
-        warp_commit(&c.bar[bEmptyY + st]);
+        if (j + 2 < chunks) warp_commit(&c.bar[bEmptyY + st]);
         const bool state = has0 || j > 0;
         if (j > 0 && !c.wait_warp(bOutFree, (j - 1) & 1)) break;
         if (state) {
@@ -920,7 +1005,7 @@ __device__ void out_mma_role(const Cta &c)
                 warp_mma_ts(dO, k < 4 ? dA + k * 8 : tmem + kColA2 + (k - 4) * 8, z + k * 128,
                             idesc_bf16(kC, DZP, false, true), state || k > 0);
         warp_commit(&c.bar[bOutFull]);
-        warp_commit(&c.bar[bEmptyZ + st]);
+        if (j + 2 < chunks) warp_commit(&c.bar[bEmptyZ + st]);
     }
     warp_commit(&c.bar[bFinOut]);
     uint32_t none = 0;
@@ -935,7 +1020,7 @@ __device__ void state_mma_role(const Cta &c)
     using L = Layout<DXP, DZP>;
     const uint32_t tmem = (uint32_t)uni((int)c.tmem);
     const uint64_t zmajor = uni(sdesc_sw128(smem_addr(c.base) + L::off_z, kSub, 1024));
-    const int updates = uni(c.updates), packed = uni(c.packed);
+    const int updates = uni(c.updates), chunks = uni(c.chunks), packed = uni(c.packed);
 #pragma unroll 1
     for (int i = 0; i < updates; ++i) {
         const int st = i & 1, live = uni(c.live<REV>(i));
@@ -950,11 +1035,11 @@ __device__ void state_mma_role(const Cta &c)
             if (!(ok = c.wait_warp(bYReady + (qd & 1), qd >> 1))) break;
             tc_fence_after();
             state_mmas<DZP>(tmem + kColB, tmem + kColY + 64 * (qd & 1), z + qd * 256, live - 32 * qd, qd == 0);
-            warp_commit(&c.bar[bYFree + (qd & 1)]);
+            if (i + 1 < updates || qd < 2) warp_commit(&c.bar[bYFree + (qd & 1)]);
         }
         if (!ok) break;
         warp_commit(&c.bar[bBFull]);
-        warp_commit(&c.bar[bEmptyZ + st]);
+        if (i + 2 < chunks) warp_commit(&c.bar[bEmptyZ + st]);
     }
     warp_commit(&c.bar[bFinState]);
     uint32_t none = 0;
@@ -973,7 +1058,7 @@ __device__ __forceinline__ void score_half(const Cta &c, int warp, int half, int
     const int lane = threadIdx.x & 31, r = 32 * warp + lane;
     const uint32_t tA = c.tmem + ((uint32_t)(32 * warp) << 16);
     const int run = REV ? 32 - r : 128 - r;                          // table entry of column 0
-    const uint32_t w0 = c.mild ? c.columns : c.powers + 4 * ((run & 1) * kPowers + (run & ~1));
+    const uint32_t w0 = c.mild ? c.columns() : c.powers() + 4 * ((run & 1) * kPowers + (run & ~1));
 #pragma unroll 1
     for (int n = 0; n < 2; ++n) {
         const int b = 2 * half + n;
@@ -1024,7 +1109,7 @@ __device__ void out_role(const Cta &c, __nv_bfloat16 *out, int H, int Dz)
     using L = Layout<DXP, DZP>;
     const int warp = (threadIdx.x >> 5) - kOutWarp, lane = threadIdx.x & 31, r = 32 * warp + lane;
     const uint32_t tO = c.tmem + ((uint32_t)(32 * warp) << 16) + kColO;
-    const float w = c.mild ? lds(power_at<REV>(c.powers, REV ? 127 - r : r + 1)) : 1.f;
+    const float w = c.mild ? lds(power_at<REV>(c.powers(), REV ? 127 - r : r + 1)) : 1.f;
     const uint64_t ww = pair(w, w);
 #pragma unroll 1
     for (int j = 0; j < c.chunks; ++j) {
@@ -1091,8 +1176,8 @@ __device__ void store_role(const Cta &c, const CUtensorMap *mo)
 }
 
 // ------------------------------------------------------------------ weighted keys and state
-template <int DXP, int DZP, bool REV>
-__device__ __forceinline__ void state_role(const Cta &c, const Params &p)
+template <int DXP, int DZP, bool REV, bool SHARED>
+__device__ __forceinline__ void state_role(const Cta &c, const Params &p, const Share &w)
 {
     using L = Layout<DXP, DZP>;
     State<DXP, DZP, REV> e(c, p, 0);
@@ -1102,7 +1187,9 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
     // the state entering the segment; the segments' own states are of the
     // launch before this one
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (c.last_rank == 0 || c.chunks == 0) {
+    if (SHARED && c.piece->from >= 0) {
+        e.take_over(w);
+    } else if (c.last_rank == 0 || c.chunks == 0) {
         if (p.init) e.load(p.init);
     } else if (c.g.rank == first_rank) {
         if (p.init) e.add_part(REV ? 0 : p.P - 1, 1.f);
@@ -1177,27 +1264,53 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
         tc_fence_before();
         arrive_warp(&c.bar[bBFree]);
     }
-    if (p.fin && c.g.rank == (REV ? 0 : c.last_rank)) e.store(p.fin);
+    if (SHARED && c.piece->to >= 0) e.hand_over(w);
+    else if (p.fin && c.g.rank == (REV ? 0 : c.last_rank)) e.store(p.fin);
 }
 
-template <int DXP, int DZP, bool REV>
-__device__ __forceinline__ void body(uint8_t *smem, const CUtensorMap *mx, const CUtensorMap *my,
+// TMEM is taken once for all of a CTA's pieces: a CTA may not allocate again
+// after it has given up the right to.
+__device__ __forceinline__ uint32_t *tmem_slot(uint8_t *smem) { return (uint32_t *)(smem + kAuxTicket + 4); }
+__device__ __forceinline__ void take_tmem(uint8_t *smem)
+{
+    if ((threadIdx.x >> 5) == kStateMmaWarp) tmem_alloc(tmem_slot(smem), kTmemCols);
+}
+__device__ __forceinline__ void give_tmem(uint8_t *smem)
+{
+    if ((threadIdx.x >> 5) != kStateMmaWarp) return;
+    __syncwarp();
+    tmem_dealloc(*(volatile uint32_t *)tmem_slot(smem), kTmemCols);
+}
+
+// a CTA's piece, in shared memory: registers are short
+__device__ __forceinline__ volatile Piece *piece_at(uint8_t *smem) { return (volatile Piece *)(smem + kAuxPiece); }
+
+template <int DXP, int DZP, bool REV, bool SHARED>
+__device__ __forceinline__ bool body(uint8_t *smem, const CUtensorMap *mx, const CUtensorMap *my,
                                      const CUtensorMap *mz, const CUtensorMap *mo, const Params &p,
-                                     __nv_bfloat16 *out, unsigned job)
+                                     __nv_bfloat16 *out, unsigned job, const Share &share)
 {
     Cta c;
     c.g = la_segment(p.cu, p.N, p.T, p.H, p.max_T, p.P, kC, job);
+    c.piece = piece_at(smem);
+    if (SHARED) {
+        const int a = (REV ? share.chunks - c.piece->b : c.piece->a) * kC;
+        const int b = (REV ? share.chunks - c.piece->a : c.piece->b) * kC;
+        c.g.begin = a;
+        c.g.end = b < c.g.len ? b : c.g.len;
+    }
     if (!c.g.ok) {
         if (threadIdx.x == 0 && c.g.h == 0 && c.g.rank == 0) report_bad_sequence(p.status);
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        return;
+        return false;
     }
-    uint32_t *slot = setup<REV>(c, p, smem);
-    if (misplaced(c)) return;
-    c.has0 = p.init != nullptr || (REV ? c.g.rank < c.last_rank : c.g.rank > 0);
-    c.updates = c.chunks - (p.fin && c.g.rank == (REV ? 0 : c.last_rank) ? 0 : 1);
+    setup<REV>(c, p, smem);
+    if (misplaced(c)) return false;
+    c.has0 = p.init != nullptr || (SHARED && c.piece->from >= 0) || (REV ? c.g.rank < c.last_rank : c.g.rank > 0);
+    c.updates = c.chunks - ((SHARED && c.piece->to >= 0) || (p.fin && c.g.rank == (REV ? 0 : c.last_rank)) ? 0 : 1);
     if (threadIdx.x < kBars) {
         const int i = threadIdx.x;
+        if (SHARED) mbar_inval(&c.bar[i]);
         mbar_init(&c.bar[i], i == bOutFree || i == bStaged                     ? kOutWarps
                              : i == bAReady                                    ? 2 * kOutWarps
                              : i == bYReady || i == bYReady + 1                ? kStateWarps / 2
@@ -1208,14 +1321,15 @@ __device__ __forceinline__ void body(uint8_t *smem, const CUtensorMap *mx, const
         fence_mbar_init();
     }
     const int warp = uni((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    if (warp == kStateMmaWarp) tmem_alloc(slot, kTmemCols);
+    if (!SHARED) take_tmem(smem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    c.tmem = *slot;
+    c.tmem = *(volatile uint32_t *)tmem_slot(smem);
+    if (SHARED) fresh_tables(c);
 
     if (warp < kScoreWarp) {
-        state_role<DXP, DZP, REV>(c, p);
+        state_role<DXP, DZP, REV, SHARED>(c, p, share);
     } else if (warp < kOutWarp) {
         score_role<REV>(c);
     } else if (warp < kLoadWarp) {
@@ -1230,39 +1344,95 @@ __device__ __forceinline__ void body(uint8_t *smem, const CUtensorMap *mx, const
     }
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
-    if (threadIdx.x == 0 && *c.abort && c.status) atomicCAS(c.status, 0u, (uint32_t)kDevTimeout);
-    if (warp == kStateMmaWarp) tmem_dealloc(c.tmem, kTmemCols);
+    const bool stop = __syncthreads_or(*c.abort != 0);
+    if (threadIdx.x == 0 && stop && c.status) atomicCAS(c.status, 0u, (uint32_t)kDevTimeout);
+    if (!SHARED) give_tmem(smem);
+    return !stop;
 }
 
-template <int DXP, int DZP, bool REV>
+// The start of a CTA that takes a share of a line: its TMEM, and its place in
+// the order of the starts.
+__device__ __forceinline__ void start(const Share &w, uint8_t *smem)
+{
+    take_tmem(smem);
+    if (threadIdx.x == 0) {
+        volatile unsigned *t = (volatile unsigned *)(smem + kAuxTicket);
+        t[0] = atomicAdd(w.flags, 1u);
+        t[2] = 0;
+    }
+    // each piece replaces the barriers by its own
+    if (threadIdx.x < kBars) mbar_init((uint64_t *)smem + threadIdx.x, 1);
+}
+// The next piece; false: none.
+__device__ __forceinline__ bool next_piece(const Share &w, uint8_t *smem)
+{
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        volatile unsigned *t = (volatile unsigned *)(smem + kAuxTicket);
+        Piece p = {};
+        do {
+            p.ok = next_piece(w, t[0], (int)t[2], &p);
+            t[2] = t[2] + 1;
+        } while (p.ok && p.block >= w.blocks);
+        volatile Piece *q = piece_at(smem);
+        q->block = p.block;
+        q->a = p.a;
+        q->b = p.b;
+        q->from = p.from;
+        q->to = p.to;
+        q->ok = p.ok;
+    }
+    __syncthreads();
+    return piece_at(smem)->ok;
+}
+
+template <int DXP, int DZP, bool REV, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
 la_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
              const __grid_constant__ CUtensorMap mz, const __grid_constant__ CUtensorMap mo, const Params p,
-             __nv_bfloat16 *out)
+             __nv_bfloat16 *out, const __grid_constant__ Share w)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
-    body<DXP, DZP, REV>(smem, &mx, &my, &mz, &mo, p, out, blockIdx.x);
+    if (!SHARED) {
+        body<DXP, DZP, REV, false>(smem, &mx, &my, &mz, &mo, p, out, blockIdx.x, w);
+        return;
+    }
+    start(w, smem);
+    while (next_piece(w, smem) && body<DXP, DZP, REV, SHARED>(smem, &mx, &my, &mz, &mo, p, out, piece_at(smem)->block, w))
+        ;
+    give_tmem(smem);
 }
 
-template <int DKP, int DVP>
+template <int DKP, int DVP, bool SHARED>
+__device__ __forceinline__ bool grad_body(uint8_t *smem, const GradMaps &m, const GradParams &g, unsigned block,
+                                          const Share &w)
+{
+    unsigned job;
+    const int pass = g.pass_of(block, g.p[0].P, &job);
+    if (pass == 0) return body<DVP, DKP, false, SHARED>(smem, &m.d, &m.v, &m.k, &m.dq, g.p[0], g.out[0], job, w);
+    if (DKP == DVP) {
+        const bool k = pass == 1;
+        return body<DKP, DVP, true, SHARED>(smem, k ? &m.v : &m.k, k ? &m.d : &m.q, k ? &m.q : &m.d,
+                                            k ? &m.dk : &m.dv, g.p[pass], g.out[pass], job, w);
+    }
+    if (pass == 1) return body<DVP, DKP, true, SHARED>(smem, &m.v, &m.d, &m.q, &m.dk, g.p[1], g.out[1], job, w);
+    return body<DKP, DVP, true, SHARED>(smem, &m.k, &m.q, &m.d, &m.dv, g.p[2], g.out[2], job, w);
+}
+
+template <int DKP, int DVP, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
-la_grad_kernel(const __grid_constant__ GradMaps m, const __grid_constant__ GradParams g)
+la_grad_kernel(const __grid_constant__ GradMaps m, const __grid_constant__ GradParams g,
+               const __grid_constant__ Share w)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
-    unsigned job;
-    const int pass = g.pass_of(blockIdx.x, g.p[0].P, &job);
-    if (pass == 0) {
-        body<DVP, DKP, false>(smem, &m.d, &m.v, &m.k, &m.dq, g.p[0], g.out[0], job);
-    } else if (DKP == DVP) {
-        const bool k = pass == 1;
-        body<DKP, DVP, true>(smem, k ? &m.v : &m.k, k ? &m.d : &m.q, k ? &m.q : &m.d, k ? &m.dk : &m.dv, g.p[pass],
-                             g.out[pass], job);
-    } else if (pass == 1) {
-        body<DVP, DKP, true>(smem, &m.v, &m.d, &m.q, &m.dk, g.p[1], g.out[1], job);
-    } else {
-        body<DKP, DVP, true>(smem, &m.k, &m.q, &m.d, &m.dv, g.p[2], g.out[2], job);
+    if (!SHARED) {
+        grad_body<DKP, DVP, false>(smem, m, g, blockIdx.x, w);
+        return;
     }
+    start(w, smem);
+    while (next_piece(w, smem) && grad_body<DKP, DVP, SHARED>(smem, m, g, piece_at(smem)->block, w))
+        ;
+    give_tmem(smem);
 }
 
 bool rows_map(CUtensorMap *map, const void *base, int D, const LaPass &p)
@@ -1278,6 +1448,40 @@ Params params_of(const LaPass &p)
 {
     return Params{p.N, p.T, p.H, p.Dx, p.Dz, p.max_T, p.P, p.log_decay, p.init, p.fin, p.part, p.cu, p.status,
                   p.state_t ? 1 : 0};
+}
+
+// Runs of neighbouring heads (and of both reverse passes of a head) stay side
+// by side: their rows are neighbours in memory, pieces of 128 or 256 bytes.
+constexpr int kWidth = 8;
+constexpr double kGradCost = 1.2;
+
+// The runs' line and its shares, in the workspace of `p` (P is 1), where that
+// ends sooner than whole runs in waves. `cost`: of a chunk in a share against
+// one in a wave; about four chunks' time goes into clearing the flags, into
+// cutting and into uneven CTAs. The gradients' CTAs share rows in L2 with
+// others, which shares set apart in time: 1.2 for them, 1 forward. Measured,
+// 128 x 128, us in waves / in shares: forward 192 heads of 20 chunks 138 / 117,
+// of 8 chunks 69 / 69, 256 of 32 212 / 204; gradients of 64 heads of 64 chunks
+// 400 / 307, of 256 heads of 32 chunks 622 / 630 (so in waves).
+cudaError_t shares(const LaPass &p, size_t blocks, double cost, size_t *grid, Share *w)
+{
+    memset(w, 0, sizeof(*w));
+    w->blocks = (unsigned)blocks;
+    w->width = kWidth;
+    w->chunks = (p.T + kC - 1) / kC;
+    *grid = blocks;
+    if (p.P > 1 || p.cu || p.shares < kWidth || w->chunks == 0) return cudaSuccess;
+    const long long ctas = p.shares / kWidth, runs = (blocks + kWidth - 1) / kWidth;
+    if (runs <= ctas) return cudaSuccess;
+    const long long waves = (runs + ctas - 1) / ctas, line = runs * w->chunks, per = (line + ctas - 1) / ctas;
+    if (cost * per + 4 >= waves * w->chunks) return cudaSuccess;
+    w->line = line;
+    w->per = per;
+    w->cells = la_part_cells(p.Dx, p.Dz);
+    w->flags = (uint32_t *)p.part;
+    w->slots = p.part + kLaShareFlags;
+    *grid = ctas * kWidth;
+    return cudaMemsetAsync(w->flags, 0, (1 + *grid) * sizeof(uint32_t), p.stream);
 }
 
 // `after`: the kernel's CTAs may start, and load their first rows, while the
@@ -1311,8 +1515,12 @@ cudaError_t launch_forward(const LaPass &p, const CUtensorMap (&m)[4])
                                      seg::Layout<DXP, DZP>::bytes, false, p.stream, m[1], m[2], pr);
         if (e != cudaSuccess) return e;
     }
-    return launch(la_tc_kernel<DXP, DZP, false>, heads * p.P, kThreads, Layout<DXP, DZP>::bytes, p.P > 1, p.stream,
-                  m[0], m[1], m[2], m[3], pr, (__nv_bfloat16 *)p.out);
+    Share w;
+    size_t grid;
+    const cudaError_t e = shares(p, heads * p.P, 1.0, &grid, &w);
+    if (e != cudaSuccess) return e;
+    return launch(w.per > 0 ? la_tc_kernel<DXP, DZP, false, true> : la_tc_kernel<DXP, DZP, false, false>, grid, kThreads, Layout<DXP, DZP>::bytes, p.P > 1, p.stream, m[0],
+                  m[1], m[2], m[3], pr, (__nv_bfloat16 *)p.out, w);
 }
 
 template <int DKP, int DVP>
@@ -1334,7 +1542,11 @@ cudaError_t launch_passes(const LaPass (&p)[3], const GradMaps &m, int first_rev
                                      a > b ? a : b, false, p[0].stream, m, g);
         if (e != cudaSuccess) return e;
     }
-    return launch(la_grad_kernel<DKP, DVP>, heads * P * passes, kThreads, c > d ? c : d, P > 1, p[0].stream, m, g);
+    Share w;
+    size_t grid;
+    const cudaError_t e = shares(p[0], heads * P * passes, kGradCost, &grid, &w);
+    if (e != cudaSuccess) return e;
+    return launch(w.per > 0 ? la_grad_kernel<DKP, DVP, true> : la_grad_kernel<DKP, DVP, false>, grid, kThreads, c > d ? c : d, P > 1, p[0].stream, m, g, w);
 }
 
 template <int DKP, int DVP>
@@ -1368,6 +1580,10 @@ int la_tc_segments(int N, int H, int T, int max_T, bool packed, int passes, int 
             t = (load > seg ? load : seg) * (P > 1 ? 1.5 : 1.0) + (P > 1 ? 3.7 : 3.0) * heads * P / sms;
         } else {
             t = ceil(heads * P / sms) * (seg + 1.5);
+            if (P == 1 && heads > sms) {   // in shares
+                const double s = (passes > 1 ? kGradCost : 1.0) * heads * chunks / sms + 4;
+                if (s < t) t = s;
+            }
             if (P > 1) t += ceil(heads * (P - 1) / sms) * (0.5 * seg + 1.5) + 1;
         }
         if (P == 1 || t < least) {

@@ -383,3 +383,35 @@ def test_states_over_one_another(dp, T, H):
         assert rc == 0
         dp.check_status(ws)
         check_backward(x, None, g)
+
+
+@pytest.mark.parametrize("T,Dk,Dv", [(2600, 64, 64), (2561, 128, 128), (2688, 32, 128)], ids=str)
+def test_runs_shared_out(dp, T, Dk, Dv):
+    # 171 heads of 21 chunks: whole runs would need a second wave, so they are
+    # cut into equal shares. Sequences 3-8 repeat 0-2, cut at other places; a
+    # cut hands the state on as it is, so they repeat the results bit for bit.
+    three = draw((3, T, 19), Dk, Dv, torch.bfloat16, T, 3, first=2)
+    x = {n: t if n == "log_decay" else t.repeat(3, *[1] * (t.dim() - 1)) for n, t in three.items()}
+    c = {n: t.cuda() for n, t in x.items()}
+    rows = (c["q"], c["k"], c["v"], c["log_decay"])
+    state = c["h0"].clone()
+    o, hf = dp.linear_attention(*rows, state, h_final=state)
+    g = dp.linear_attention_backward(*rows, c["h0"], d_o=c["d_o"], dh_final=c["dh"])
+    # the same with dh0 over dh_final: other launches, other cuts
+    from deltaproduct_householder_product_gb300 import _lib
+    dims = _lib.make_la_dims(9, T, 19, Dk, Dv, torch.bfloat16)
+    ws = torch.zeros(dp.linear_attention_workspace_size(9, T, 19, Dk, Dv, dtype=torch.bfloat16, backward=True),
+                     dtype=torch.uint8, device="cuda")
+    over = {n: torch.empty_like(g[n]) for n in ("dq", "dk", "dv")} | {"dh0": c["dh"].clone()}
+    p = _lib._ptr
+    rc = _lib.lib().dp_linear_attention_backward(
+        dims, *map(p, rows), p(c["h0"]), p(c["d_o"]), p(over["dh0"]), p(over["dq"]), p(over["dk"]), p(over["dv"]),
+        p(over["dh0"]), p(ws), ws.numel(), _lib._stream(None))
+    assert rc == 0
+    dp.check_status(ws)
+    for n, t in [("o", o), ("h_final", hf)] + list(g.items()):
+        assert torch.equal(t[:3], t[3:6]) and torch.equal(t[:3], t[6:]), n
+    for n in g:
+        assert torch.equal(g[n], over[n]), n
+    check_forward(three, None, o[:3], hf[:3])
+    check_backward(three, None, {n: t[:3] for n, t in g.items()})
