@@ -986,10 +986,16 @@ Form form_of(const GroupNorm &p, bool grad)
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
-// row-form CTAs along the rows: enough to fill the SMs several times over,
-// each with rows to walk
-int row_ctas(const GroupNorm &p, const RowMap &m, int per_sm)
+// Row-form CTAs along the rows: as many as the SMs hold at once by their
+// registers, each with rows to walk (a second wave of shorter walks would load
+// the weights, and leave channel sums, again). bf16, us at 32768 x 2048 in
+// groups of 128 and at 8192 x 1024: forward 49.5 and 8.1 with 3 an SM, 51.2 and
+// 10.2 with 8, 55 and 8.8 with 2; gradients 104 and 18.1 with 2, 129 and 24.3
+// with 3, 110 and 21.5 with 4. fp32, 16384 x 2048: 53.5 with 8, 56.2 with 3;
+// gradients 102.8 with 4, 120.7 with 2.
+int row_ctas(const GroupNorm &p, const RowMap &m, bool grad)
 {
+    const int per_sm = p.dtype == DP_F32 ? (grad ? 4 : 8) : (grad ? 2 : 3);
     const long long most = ceil_div(p.N, m.per), cols = ceil_div(m.slots, kThreads);
     const long long want = 152ll * per_sm / (m.per > 1 ? 1 : cols);
     return (int)(want < 1 ? 1 : want < most ? want : most);
@@ -1060,7 +1066,7 @@ cudaError_t forward_typed(const GroupNorm &p)
     switch (form_of(p, false)) {
     case kFormRows: {
         const RowMap m = row_map(p, K, 2);
-        const dim3 grid(row_ctas(p, m, 8), m.per > 1 ? 1 : ceil_div(m.slots, kThreads));
+        const dim3 grid(row_ctas(p, m, false), m.per > 1 ? 1 : ceil_div(m.slots, kThreads));
         const int v = ceil_div(m.pieces, m.lanes);
         if (v == 1) gn_rows_kernel<T, 1, ACT><<<grid, kThreads, 0, p.stream>>>(p, m);
         else if (v == 2) gn_rows_kernel<T, 2, ACT><<<grid, kThreads, 0, p.stream>>>(p, m);
@@ -1090,7 +1096,7 @@ cudaError_t backward_typed(const GroupNorm &p)
     switch (form_of(p, true)) {
     case kFormRows: {
         const RowMap m = row_map(p, K, 1);
-        const int ctas = row_ctas(p, m, 4);
+        const int ctas = row_ctas(p, m, true);
         const dim3 grid(ctas, m.per > 1 ? 1 : ceil_div(m.slots, kThreads));
         float *part = sums ? p.scratch : nullptr;
         if (ceil_div(m.pieces, m.lanes) == 1) gn_rows_backward_kernel<T, 1, ACT><<<grid, kThreads, 0, p.stream>>>(p, m, part);
@@ -1139,7 +1145,7 @@ size_t gn_backward_scratch_bytes(const GroupNorm &p)
     if (p.N == 0) return 0;
     const int vec = p.dtype == DP_F32 ? 4 : 8;
     switch (form_of(p, true)) {
-    case kFormRows: return (size_t)row_ctas(p, row_map(p, vec, 1), 4) * 2 * p.C * sizeof(float);
+    case kFormRows: return (size_t)row_ctas(p, row_map(p, vec, 1), true) * 2 * p.C * sizeof(float);
     case kFormPositions:
         return (position_part_values(p, position_map(p, vec, kPerSmGrad)) + 2 * (size_t)p.N * p.G) * sizeof(float);
     default: return (size_t)channel_slices(p) * 2 * p.C * sizeof(float);
