@@ -1326,10 +1326,26 @@ __device__ __forceinline__ void give_tmem(uint8_t *smem)
     tmem_dealloc(*(volatile uint32_t *)tmem_slot(smem), kTmemCols);
 }
 
+// Registers move between the warpgroups: 896 threads start with 72 each; the
+// four warps of loads, MMAs and stores leave 32 each to the state's sixteen
+// (128 x 32 = 512 x 8), and both go back at the end. For states of 128 x 128,
+// which spill without: forward of 4 x 64 heads of 4096 rows 204 -> 199 us,
+// gradients in shares of 4 x 16 heads of 8192 rows 306 -> 291. Smaller states
+// gain nothing (packed, 64 x 64: 71 -> 72), and gradients of many short
+// sequences lost (200 of 64 rows, 8 heads: 356 -> 489), so those do without.
+template <int N> __device__ __forceinline__ void more_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void fewer_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // a CTA's piece, in shared memory: registers are short
 __device__ __forceinline__ volatile Piece *piece_at(uint8_t *smem) { return (volatile Piece *)(smem + kAuxPiece); }
 
-template <int DXP, int DZP, bool REV, bool SHARED>
+template <int DXP, int DZP, bool REV, bool SHARED, bool MOVE>
 __device__ __forceinline__ bool body(uint8_t *smem, const CUtensorMap *mx, const CUtensorMap *my,
                                      const CUtensorMap *mz, const CUtensorMap *mo, const Params &p,
                                      __nv_bfloat16 *out, unsigned job, const Share &share)
@@ -1373,18 +1389,26 @@ __device__ __forceinline__ bool body(uint8_t *smem, const CUtensorMap *mx, const
     if (SHARED) fresh_tables(c);
 
     if (warp < kScoreWarp) {
+        if (MOVE) more_registers<80>();
         state_role<DXP, DZP, REV, SHARED>(c, p, share);
+        __syncwarp();
+        if (MOVE) fewer_registers<72>();
     } else if (warp < kOutWarp) {
         score_role<REV>(c);
     } else if (warp < kLoadWarp) {
         out_role<DXP, DZP, REV>(c, out, p.H, p.Dz);
-    } else if (warp == kOutMmaWarp) {
-        out_mma_role<DXP, DZP, REV>(c);
-    } else if (warp == kStateMmaWarp) {
-        state_mma_role<DXP, DZP, REV>(c);
-    } else if (lane == 0) {
-        if (warp == kLoadWarp) load_role<DXP, DZP, REV>(c, mx, my, mz);
-        else if (warp == kStoreWarp) store_role<DXP, DZP, REV>(c, mo);
+    } else {
+        if (MOVE) fewer_registers<40>();
+        if (warp == kOutMmaWarp) {
+            out_mma_role<DXP, DZP, REV>(c);
+        } else if (warp == kStateMmaWarp) {
+            state_mma_role<DXP, DZP, REV>(c);
+        } else if (lane == 0) {
+            if (warp == kLoadWarp) load_role<DXP, DZP, REV>(c, mx, my, mz);
+            else if (warp == kStoreWarp) store_role<DXP, DZP, REV>(c, mo);
+        }
+        __syncwarp();
+        if (MOVE) more_registers<72>();
     }
     __syncwarp();
     tc_fence_before();
@@ -1436,13 +1460,14 @@ la_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
              const __grid_constant__ CUtensorMap mz, const __grid_constant__ CUtensorMap mo, const Params p,
              __nv_bfloat16 *out, const __grid_constant__ Share w)
 {
+    constexpr bool kMove = DXP == 128 && DZP == 128;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (!SHARED) {
-        body<DXP, DZP, REV, false>(smem, &mx, &my, &mz, &mo, p, out, longest_first(p, p.P, smem), w);
+        body<DXP, DZP, REV, false, kMove>(smem, &mx, &my, &mz, &mo, p, out, longest_first(p, p.P, smem), w);
         return;
     }
     start(w, smem);
-    while (next_piece(w, smem) && body<DXP, DZP, REV, SHARED>(smem, &mx, &my, &mz, &mo, p, out, piece_at(smem)->block, w))
+    while (next_piece(w, smem) && body<DXP, DZP, REV, SHARED, kMove>(smem, &mx, &my, &mz, &mo, p, out, piece_at(smem)->block, w))
         ;
     give_tmem(smem);
 }
@@ -1451,16 +1476,17 @@ template <int DKP, int DVP, bool SHARED>
 __device__ __forceinline__ bool grad_body(uint8_t *smem, const GradMaps &m, const GradParams &g, unsigned block,
                                           const Share &w)
 {
+    constexpr bool kMove = SHARED && DKP == 128 && DVP == 128;
     unsigned job;
     const int pass = g.pass_of(block, g.p[0].P, &job);
-    if (pass == 0) return body<DVP, DKP, false, SHARED>(smem, &m.d, &m.v, &m.k, &m.dq, g.p[0], g.out[0], job, w);
+    if (pass == 0) return body<DVP, DKP, false, SHARED, kMove>(smem, &m.d, &m.v, &m.k, &m.dq, g.p[0], g.out[0], job, w);
     if (DKP == DVP) {
         const bool k = pass == 1;
-        return body<DKP, DVP, true, SHARED>(smem, k ? &m.v : &m.k, k ? &m.d : &m.q, k ? &m.q : &m.d,
+        return body<DKP, DVP, true, SHARED, kMove>(smem, k ? &m.v : &m.k, k ? &m.d : &m.q, k ? &m.q : &m.d,
                                             k ? &m.dk : &m.dv, g.p[pass], g.out[pass], job, w);
     }
-    if (pass == 1) return body<DVP, DKP, true, SHARED>(smem, &m.v, &m.d, &m.q, &m.dk, g.p[1], g.out[1], job, w);
-    return body<DKP, DVP, true, SHARED>(smem, &m.k, &m.q, &m.d, &m.dv, g.p[2], g.out[2], job, w);
+    if (pass == 1) return body<DVP, DKP, true, SHARED, kMove>(smem, &m.v, &m.d, &m.q, &m.dk, g.p[1], g.out[1], job, w);
+    return body<DKP, DVP, true, SHARED, kMove>(smem, &m.k, &m.q, &m.d, &m.dv, g.p[2], g.out[2], job, w);
 }
 
 template <int DKP, int DVP, bool SHARED>
