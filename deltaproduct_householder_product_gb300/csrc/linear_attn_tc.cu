@@ -44,9 +44,9 @@
 // cycles for each barrier, complete or not). 128 rows: the largest M of one
 // MMA; longer chunks would need two tiles of scores, shorter ones as many
 // hand-overs for fewer rows. Measured at 128 x 128: forward 4 x 8 heads of 2048
-// rows 34 us, 16 heads of 32768 rows 149 us (3.6 TB/s of the rows read once,
-// 5.1 with the states' kernel's second reading), gradients of 4 x 16 heads of
-// 8192 rows 307 us (3.1 TB/s of what they cannot do without).
+// rows 34 us, 16 heads of 32768 rows 147 us (3.7 TB/s of the rows read once,
+// 5.2 with the states' kernel's second reading), gradients of 4 x 16 heads of
+// 8192 rows 297 us (3.2 TB/s of what they cannot do without).
 #include "f32x2.cuh"
 #include "linear_attn.h"
 #include "sm100.cuh"
@@ -1532,7 +1532,8 @@ constexpr double kGradCost = 1.2;
 // others, which shares set apart in time: 1.2 for them, 1 forward. Measured,
 // 128 x 128, us in waves / in shares: forward 192 heads of 20 chunks 138 / 117,
 // of 8 chunks 69 / 69, 256 of 32 212 / 204; gradients of 64 heads of 64 chunks
-// 400 / 307, of 256 heads of 32 chunks 622 / 630 (so in waves).
+// 400 / 307, of 256 heads of 32 chunks 622 / 630 (so in waves); before registers
+// moved between warpgroups, which gains either side 3-5%.
 cudaError_t shares(const LaPass &p, size_t blocks, double cost, size_t *grid, Share *w)
 {
     memset(w, 0, sizeof(*w));
