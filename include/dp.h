@@ -328,8 +328,9 @@ typedef struct {
 
 /* Bytes of device workspace of the calls below (>= 256; the status block,
  * then the states of the segments that a sequence is cut into where few
- * sequences and heads would leave SMs idle). It depends on dims and on the
- * current device. Calls sharing a workspace must be ordered (one stream);
+ * sequences and heads would leave SMs idle, or the states that one CTA hands
+ * to the next where there are more sequences and heads than SMs). It depends
+ * on dims and on the current device. Calls sharing a workspace must be ordered (one stream);
  * contents need not be kept between calls, except for the status word. */
 dp_status dp_linear_attention_workspace_size(const dp_la_dims *dims, size_t *bytes);
 dp_status dp_linear_attention_backward_workspace_size(const dp_la_dims *dims, size_t *bytes);
