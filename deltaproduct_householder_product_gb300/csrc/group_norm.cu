@@ -146,8 +146,21 @@ template <typename T> struct Raw<T, 1> {
 // sum over the `lanes` (a power of two) neighbouring lanes of a group
 __device__ __forceinline__ float lane_sum(float v, int lanes)
 {
-    for (int m = lanes >> 1; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1)
+        if (m < lanes) v += __shfl_xor_sync(0xffffffffu, v, m);
     return v;
+}
+// two at once: one's steps cover the other's latency
+__device__ __forceinline__ void lane_sums(float &a, float &b, int lanes)
+{
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1)
+        if (m < lanes) {
+            const float x = __shfl_xor_sync(0xffffffffu, a, m), y = __shfl_xor_sync(0xffffffffu, b, m);
+            a += x;
+            b += y;
+        }
 }
 
 // sums over the CTA, the same in every thread
@@ -257,7 +270,7 @@ gn_rows_kernel(GroupNorm p, RowMap m)
                     sq = fma2(x[v][k], x[v][k], sq);
                 }
         unpair(sq, s0, s1);
-        const float rstd = 1.f / sqrtf(fmaf(lane_sum(s0 + s1, m.lanes), inv, p.eps));
+        const float rstd = rsqrtf(fmaf(lane_sum(s0 + s1, m.lanes), inv, p.eps));   // 2 ulp
         if (!row) continue;
         const uint64_t rr = pair(rstd, rstd);
 #pragma unroll
@@ -360,12 +373,12 @@ gn_rows_backward_kernel(GroupNorm p, RowMap m, float *part)
                     su = add2(su, u[v][k]);
                     suh = fma2(u[v][k], h[v][k], suh);
                 }
-        float s0, s1;
+        float s0, s1, h0, h1;
         unpair(su, s0, s1);
-        const float mu = lane_sum(s0 + s1, m.lanes) * inv;
-        unpair(suh, s0, s1);
-        const float muh = lane_sum(s0 + s1, m.lanes) * inv;
-        const uint64_t a = pair(-mu, -mu), c = pair(-muh, -muh);
+        unpair(suh, h0, h1);
+        float mu = s0 + s1, muh = h0 + h1;
+        lane_sums(mu, muh, m.lanes);
+        const uint64_t a = pair(-mu * inv, -mu * inv), c = pair(-muh * inv, -muh * inv);
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (on[v] && row) {
