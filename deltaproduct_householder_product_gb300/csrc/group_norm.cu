@@ -17,8 +17,9 @@
 //             channels; partial sums, then a second walk over the rows, which
 //             L2 serves where the tensor fits.
 //  wide       S = 1, what is left (very wide groups or rows): a CTA per group.
-// Measured, bf16 with SiLU: rows 32768 x 2048 in 16 groups 49.5 us (5.5 TB/s,
-// 73% of the issue slots), gradients 104 us (3.9 TB/s); positions 4 x 4099 x 640
+// Measured, bf16 with SiLU: rows 32768 x 2048 in 16 groups 46.7 us (5.7 TB/s),
+// gradients 99 us (4.1 TB/s: 16 warps an SM, which the registers for weights
+// and channel sums allow); positions 4 x 4099 x 640
 // in 32 groups 21 us, gradients 28 us (both tensors in L2).
 // Squared distances are taken from the mean (or summed about a nearby value
 // and combined by counts, means and squares), never as E[x^2] - mean^2.
@@ -1004,7 +1005,8 @@ int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // Row-form CTAs along the rows: as many as the SMs hold at once by their
 // registers, each with rows to walk (a second wave of shorter walks would load
-// the weights, and leave channel sums, again). bf16, us at 32768 x 2048 in
+// the weights, and leave channel sums, again). Measured a step earlier, all 5-10%
+// faster since: bf16, us at 32768 x 2048 in
 // groups of 128 and at 8192 x 1024: forward 49.5 and 8.1 with 3 an SM, 51.2 and
 // 10.2 with 8, 55 and 8.8 with 2; gradients 104 and 18.1 with 2, 129 and 24.3
 // with 3, 110 and 21.5 with 4. fp32, 16384 x 2048: 53.5 with 8, 56.2 with 3;
