@@ -1059,7 +1059,8 @@ cudaError_t forward_positions(const GroupNorm &p, const PositionMap &m)
     cudaError_t e = launch_after(gn_position_combine_kernel, dim3((unsigned)(p.N * p.G)), kThreads, p.stream, p, m,
                                  (const float *)part, mean, rstd);
     if (e != cudaSuccess) return e;
-    return launch_after(gn_position_apply_kernel<T, K, ACT>, grid, kThreads, p.stream, p, m, (const float *)mean, (const float *)rstd);
+    return launch_after(gn_position_apply_kernel<T, K, ACT>, grid, kThreads, p.stream, p, m, (const float *)mean,
+                        (const float *)rstd);
 }
 
 template <typename T, int K, int ACT>

@@ -588,7 +588,10 @@ struct State {
             uint32_t n = 0;
 #pragma unroll 1
             for (uint32_t i = 0; i < kHandTries && !*c.abort; ++i) {
-                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(w.flags + 1 + c.piece->from) : "memory");
+                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];"
+                             : "=r"(n)
+                             : "l"(w.flags + 1 + c.piece->from)
+                             : "memory");
                 if (n == kStateWarps) break;
                 __nanosleep(500);
             }
@@ -1467,7 +1470,8 @@ la_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
         return;
     }
     start(w, smem);
-    while (next_piece(w, smem) && body<DXP, DZP, REV, SHARED, kMove>(smem, &mx, &my, &mz, &mo, p, out, piece_at(smem)->block, w))
+    while (next_piece(w, smem) &&
+           body<DXP, DZP, REV, SHARED, kMove>(smem, &mx, &my, &mz, &mo, p, out, piece_at(smem)->block, w))
         ;
     give_tmem(smem);
 }
@@ -1590,8 +1594,8 @@ cudaError_t launch_forward(const LaPass &p, const CUtensorMap (&m)[4])
     size_t grid;
     const cudaError_t e = shares(p, heads * p.P, 1.0, &grid, &w);
     if (e != cudaSuccess) return e;
-    return launch(w.per > 0 ? la_tc_kernel<DXP, DZP, false, true> : la_tc_kernel<DXP, DZP, false, false>, grid, kThreads, Layout<DXP, DZP>::bytes, p.P > 1, p.stream, m[0],
-                  m[1], m[2], m[3], pr, (__nv_bfloat16 *)p.out, w);
+    return launch(w.per > 0 ? la_tc_kernel<DXP, DZP, false, true> : la_tc_kernel<DXP, DZP, false, false>, grid,
+                  kThreads, Layout<DXP, DZP>::bytes, p.P > 1, p.stream, m[0], m[1], m[2], m[3], pr, (__nv_bfloat16 *)p.out, w);
 }
 
 template <int DKP, int DVP>
@@ -1617,7 +1621,8 @@ cudaError_t launch_passes(const LaPass (&p)[3], const GradMaps &m, int first_rev
     size_t grid;
     const cudaError_t e = shares(p[0], heads * P * passes, kGradCost, &grid, &w);
     if (e != cudaSuccess) return e;
-    return launch(w.per > 0 ? la_grad_kernel<DKP, DVP, true> : la_grad_kernel<DKP, DVP, false>, grid, kThreads, c > d ? c : d, P > 1, p[0].stream, m, g, w);
+    return launch(w.per > 0 ? la_grad_kernel<DKP, DVP, true> : la_grad_kernel<DKP, DVP, false>, grid, kThreads,
+                  c > d ? c : d, P > 1, p[0].stream, m, g, w);
 }
 
 template <int DKP, int DVP>
